@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "host.cuh"
 #include "route.cuh"
 #include "bwd.cuh"
 #include "tc_gemm.cuh"
@@ -21,61 +22,6 @@
 using namespace lmoe;
 
 namespace {
-
-// ------------------------------------------------------------------ tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
-// Tensor map of a row-major matrix with a 128-byte swizzle (the layout the MMA descriptors and the
-// staged epilogue expect).
-bool make_map_t(CUtensorMap* m, const void* base, long long rows, long long cols, long long pitch, int box_rows,
-                bool f32) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const long long es_bytes = f32 ? 4 : 2;
-  if (((uintptr_t)base & 15) || ((pitch * es_bytes) & 15) || rows <= 0 || cols <= 0) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)(pitch * es_bytes)};
-  cuuint32_t box[2] = {f32 ? 32u : 64u, (cuuint32_t)box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// bf16 matrix [rows, cols], row pitch `pitch` elements; box = 64 columns (128 bytes) x box_rows.
-bool make_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long pitch, int box_rows) {
-  return make_map_t(m, base, rows, cols, pitch, box_rows, false);
-}
-// 8-bit matrix [rows, cols]; box = 128 columns (128 bytes) x box_rows, 128-byte swizzle.
-bool make_map_u8(CUtensorMap* m, const void* base, long long rows, long long cols, long long pitch, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  if (((uintptr_t)base & 15) || (pitch & 15) || rows <= 0 || cols <= 0) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)pitch};
-  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// fp32 matrix; box = 32 columns (128 bytes) x box_rows.
-bool make_map_f32(CUtensorMap* m, const void* base, long long rows, long long cols, long long pitch, int box_rows) {
-  return make_map_t(m, base, rows, cols, pitch, box_rows, true);
-}
 
 int pick_bn(int n) { return n % 256 == 0 ? 256 : (n % 128 == 0 ? 128 : 64); }
 
@@ -97,50 +43,6 @@ int pick_bn_for(long long M, int N, int sms, int min_bn) {
   for (int bn = min_bn; bn <= 256; bn <<= 1)
     if (N % bn == 0) return bn;
   return min_bn;
-}
-
-// Raises a kernel's dynamic shared-memory limit once per device; `done` is the caller's own
-// per-kernel flag word (one bit per device).
-template <typename K>
-cudaError_t ensure_smem_attr(K kern, int bytes, unsigned& done) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const unsigned bit = 1u << (dev & 31);
-  if (done & bit) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done |= bit;
-  return e;
-}
-
-// Launches `kern` with programmatic stream serialisation, so its blocks may be scheduled while
-// the previous kernel of the stream drains (every kernel of the layer calls pdl_wait() before
-// touching data another kernel writes), and for cluster_x > 1 in clusters of cluster_x CTAs.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster_x,
-                     Args... args) {
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  memset(attr, 0, sizeof(attr));
-  int n = 0;
-  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[n].val.programmaticStreamSerializationAllowed = 1;
-  ++n;
-  if (cluster_x > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster_x;
-    attr[n].val.clusterDim.y = 1;
-    attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Whether a launch uses the engine's general modes (MN-major operands, per-segment B maps,
@@ -293,8 +195,6 @@ cudaError_t launch_combine(const T* o, const float* gates, const int* prow, int 
   if (k <= 6) return launch_k(combine_kernel<T, 6>, grid, block, 0, st, 1, o, gates, prow, T_, k, l, z);
   return launch_k(combine_kernel<T, 8>, grid, block, 0, st, 1, o, gates, prow, T_, k, l, z);
 }
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Stages timed by the optional per-stage profiler (lmoe_profile_enable).
 enum Stage : int {
@@ -573,11 +473,6 @@ int validate(const lmoe_config* c) {
     return LMOE_EUNSUPPORTED;
   return LMOE_OK;
 }
-
-#define CK(x)                                 \
-  do {                                        \
-    if ((x) != cudaSuccess) return LMOE_ECUDA; \
-  } while (0)
 
 int grid_1d(long long n, int threads) {
   long long b = (n + threads - 1) / threads;
