@@ -331,6 +331,86 @@ typedef struct {
 int lmoe_forward_backward(lmoe_handle *h, const lmoe_weights *w, const void *x, const void *dy, void *y,
                           int32_t T, uint32_t flags, const lmoe_grads *g, void *stream);
 
+/* ---- MXFP4: microscaled 4-bit floating point -------------------------------------------------
+ * The pages give K3's experts 4-bit weights ("Kimi K3登顶开源第一..." (cge.wang)) and fix no format;
+ * the reading here is MXFP4.  32 consecutive values along a row share a scale 2^X,
+ * X = floor(log2 max|v|) - 2 clamped to [-127, 127] (-127 for a zero block); a value is held as the
+ * E2M1 code of v 2^-X: 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign, to the nearest, ties to the even code,
+ * saturating at 6.  A block that holds a NaN or an infinity stands for 32 NaNs.
+ *
+ * A matrix of `rows` x `cols` (cols a multiple of 32, rows at most 2^30) is two caller-owned device
+ * buffers, 16-byte aligned, of the sizes lmoe_mx4_bytes gives: elements (row-major, two codes a
+ * byte, the first in the low half) and scales (UE8M0 bytes X + 127, 255 for NaN, in the order the
+ * tensor core reads them).  The scales follow the matrix's groups of rows (1 .. 1024):
+ *  - offsets NULL: `groups` groups of rows / groups rows each (1: a plain matrix; E: the stacked
+ *    weights of E experts);
+ *  - offsets [groups + 1] int32, device: group g is rows offsets[g] .. offsets[g + 1], as the
+ *    routing's offsets are (empty groups allowed).  Rows before offsets[0] and from
+ *    offsets[groups] on belong to none: they are not read.
+ * A matrix is read with the groups it was quantised with.
+ *
+ * status_dev is a caller-owned device word that the calls OR fault bits into and never clear:
+ * LMOE_STATUS_BAD_INDEX for offsets that decrease or leave [0, rows] (no group then has any rows),
+ * LMOE_STATUS_WATCHDOG for a pipeline wait that gave up.  No call allocates or synchronises, and
+ * all may be captured into a graph. */
+
+/* flags of lmoe_mx4_gemm and lmoe_mx4_dequant */
+#define LMOE_MX4_SWIGLU 1u      /* lmoe_mx4_gemm: the SwiGLU form (see there) */
+#define LMOE_MX4_ZERO_REST 2u   /* rows of the result that belong to no group are set to zero; without
+                                   it they are left as they are */
+
+/* Sizes of the element and scale buffers; `ragged` != 0: rows grouped by offsets.  Host only. */
+int lmoe_mx4_bytes(int64_t rows, int32_t cols, int32_t groups, int32_t ragged, size_t *elem_bytes,
+                   size_t *scale_bytes);
+
+/* Quantises x [rows, cols] (dtype LMOE_F32 or LMOE_BF16, `ld` elements from row to row). */
+int lmoe_mx4_quant(const void *x, int32_t dtype, int64_t ld, int64_t rows, int32_t cols, int32_t groups,
+                   const int32_t *offsets, uint8_t *elems, uint8_t *scales, uint32_t *status_dev, void *stream);
+
+/* Quantises a SwiGLU's gate and linear projections w1, w3 [groups, h, cols] (h a multiple of 64)
+ * into one matrix of 2h rows a group, interleaved as lmoe_mx4_gemm's SwiGLU form reads it: row
+ * 128 (j / 64) + j % 64 is w1's row j, 64 further w3's. */
+int lmoe_mx4_quant_w13(const void *w1, const void *w3, int32_t dtype, int32_t groups, int32_t h, int32_t cols,
+                       uint8_t *elems, uint8_t *scales, uint32_t *status_dev, void *stream);
+
+/* The values a matrix stands for, into out [rows, cols] (`ld` elements from row to row).  bf16 and
+ * fp32 hold every one exactly. */
+int lmoe_mx4_dequant(const uint8_t *elems, const uint8_t *scales, int64_t rows, int32_t cols, int32_t groups,
+                     const int32_t *offsets, void *out, int32_t dtype, int64_t ld, uint32_t flags,
+                     uint32_t *status_dev, void *stream);
+
+/* C = A B^T, A [M, K] and B [groups N, K] in MXFP4, sums in fp32.
+ * groups == 1, offsets NULL: C[M, N].  offsets: row r of group g of A (quantised with the same
+ * offsets) times matrix g of B (quantised as `groups` equal groups).
+ * LMOE_MX4_SWIGLU: B's rows come in groups of 64 gate and 64 linear rows (lmoe_mx4_quant_w13; N a
+ * multiple of 128), and C[M, N / 2] (bf16) is silu(gate) * linear.
+ * c_dtype LMOE_F32 or LMOE_BF16; `ldc` elements from row to row of C.  The products are exact and
+ * sums are kept in fp32 by the tensor core; the same call gives the same bits every time. */
+int lmoe_mx4_gemm(const uint8_t *a_elems, const uint8_t *a_scales, const uint8_t *b_elems, const uint8_t *b_scales,
+                  int32_t M, int32_t N, int32_t K, int32_t groups, const int32_t *offsets, void *c, int32_t c_dtype,
+                  int64_t ldc, uint32_t flags, uint32_t *status_dev, void *stream);
+
+/* ---- Balance loss of a router ----------------------------------------------------------------
+ * An auxiliary loss beside the bias updates, sequence by sequence.  Sequence q is tokens
+ * cu_seqlens[q] .. cu_seqlens[q + 1] (int32 device, [S + 1]; NULL with S == 1: all T tokens); S' of
+ * the S hold tokens.  From the router's scores s [T, E] (as lmoe_get_routing gives them) and choice
+ * idx [T, k] (-1: a slot that chose none):
+ *   counts[q, e] = (token, slot) pairs of sequence q that chose expert e
+ *   L = coef / S' sum_q sum_e f_qe mean_{t in q} (s_te / sum_j s_tj),   f_qe = counts[q, e] E / (k n_q)
+ * for n_q tokens in q, and, when dscores [T, E] is given, its gradient dL/ds.  The choice is
+ * piecewise constant: no gradient flows through the counts.  A token outside every sequence takes
+ * no part and gets a zero gradient; so does a token whose scores are all zero.  A NaN score makes the
+ * loss and its token's gradient NaN and sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index
+ * other than -1 outside [0, E) is not counted, and it, or cu_seqlens that decrease or leave [0, T],
+ * sets LMOE_STATUS_BAD_INDEX (the bits are ORed in, never cleared).
+ * E at most 1024, k at most 32.  scratch is lmoe_balance_scratch_bytes of device memory, 16-byte
+ * aligned, the call's own until it has run.  Sums are taken in a fixed order: the same call gives
+ * the same bits every time. */
+int lmoe_balance_scratch_bytes(size_t *bytes);
+int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_t E, int32_t k,
+                      const int32_t *cu_seqlens, int32_t S, float coef, int32_t *counts, float *loss, float *dscores,
+                      void *scratch, uint32_t *status_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

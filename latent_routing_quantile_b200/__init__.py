@@ -22,6 +22,8 @@ UPDATE_BIAS = 4
 ASYNC_OUTPUT = 8
 QB_LITERAL = 1
 BIAS_SIGN = 2
+MX4_SWIGLU = 1
+MX4_ZERO_REST = 2
 STATUS_NAN_SCORE, STATUS_WATCHDOG, STATUS_BAD_INDEX = 1, 2, 4
 NBINS = 4096
 
@@ -31,6 +33,8 @@ EXPORTED = (
     "lmoe_get_hist", "lmoe_set_hist", "lmoe_get_load", "lmoe_set_load", "lmoe_get_status", "lmoe_strerror", "lmoe_gemm_bf16",
     "lmoe_profile_enable", "lmoe_profile_read", "lmoe_stage_name", "lmoe_launch_count",
     "lmoe_route_noalloc", "lmoe_watchdog_selftest", "lmoe_gemm_bf16_ex", "lmoe_forward_backward",
+    "lmoe_mx4_bytes", "lmoe_mx4_quant", "lmoe_mx4_quant_w13", "lmoe_mx4_dequant", "lmoe_mx4_gemm",
+    "lmoe_balance_scratch_bytes", "lmoe_balance_loss",
 )
 NUM_STAGES = 14
 
@@ -65,7 +69,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise LmoeError(f"{LIB_PATH} is missing: build it with `python -m latent_routing_quantile_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i32, u32 = c_void_p, c_int32, c_uint32
+        vp, i32, u32, i64 = c_void_p, c_int32, c_uint32, ctypes.c_int64
         sig = {
             "lmoe_create": [POINTER(lmoe_config), POINTER(lmoe_weights), vp, POINTER(vp)],
             "lmoe_destroy": [vp],
@@ -92,6 +96,13 @@ def lib() -> ctypes.CDLL:
             "lmoe_launch_count": [vp, POINTER(ctypes.c_int64)],
             "lmoe_route_noalloc": [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp],
             "lmoe_watchdog_selftest": [vp, i32, vp],
+            "lmoe_mx4_bytes": [i64, i32, i32, i32, POINTER(c_size_t), POINTER(c_size_t)],
+            "lmoe_mx4_quant": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp, vp],
+            "lmoe_mx4_quant_w13": [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp],
+            "lmoe_mx4_dequant": [vp, vp, i64, i32, i32, vp, vp, i32, i64, u32, vp, vp],
+            "lmoe_mx4_gemm": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i64, u32, vp, vp],
+            "lmoe_balance_scratch_bytes": [POINTER(c_size_t)],
+            "lmoe_balance_loss": [vp, vp, i32, i32, i32, vp, i32, c_float, vp, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -443,6 +454,254 @@ def route_noalloc(scores, bias, k, out=None, stream=None):
                                     *(_ptr(out[n]) for n in ("idx", "gates", "counts", "offsets", "perm", "inv",
                                                              "status")),
                                     _stream(stream)), "lmoe_route_noalloc")
+    return out
+
+
+# --------------------------------------------------------------------------- operators on the caller's tensors
+_status_words = {}
+
+
+def _status_word(dev):
+    """The device word that the operators below OR their fault bits into (one a device)."""
+    if dev not in _status_words:
+        if torch.cuda.is_current_stream_capturing():
+            raise LmoeError("the first operator call on a device cannot be captured: make one before the capture")
+        _status_words[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
+        torch.cuda.synchronize(dev)
+    return _status_words[dev]
+
+
+def op_status(device=None) -> int:
+    """Fault bits (STATUS_*) of the mx4_* and balance_loss calls on `device` since the last read;
+    synchronises the device and clears them."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if dev not in _status_words:
+        return 0
+    torch.cuda.synchronize(dev)
+    v = int(_status_words[dev].item()) & 0xffffffff
+    _status_words[dev].zero_()
+    torch.cuda.synchronize(dev)
+    return v
+
+
+class _OnDevice:
+    """Runs an operator on the device of its tensors: makes that device and the call's stream
+    current (new tensors then belong to that stream), and tells torch that the tensors are in use
+    there when the caller names a stream of its own."""
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        if dev.type != "cuda":
+            raise LmoeError("tensors must be CUDA tensors")
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise LmoeError(f"tensors on different devices ({dev} and {t.device})")
+        if stream is not None and stream.device != dev:
+            raise LmoeError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.dev, self.named = dev, stream is not None
+        self.stream = stream if self.named else torch.cuda.current_stream(dev)
+        self.tensors = tensors
+        self.ctx = None
+        if self.named or torch.cuda.current_device() != dev.index:
+            self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        self.status = _status_word(self.dev)
+        return self
+
+    def __exit__(self, *exc):
+        if self.named:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+    @property
+    def ptr(self):
+        return c_void_p(self.stream.cuda_stream)
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _dtype(dtype, name):
+    if dtype not in _DTYPES:
+        raise LmoeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _offsets(offsets):
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise LmoeError("offsets must be a contiguous int32 tensor of one dimension, groups + 1 long")
+    return offsets
+
+
+class Mx4:
+    """A matrix in MXFP4 (see lmoe.h): `rows` x `cols` in `groups` groups of rows, equal ones or those
+    of `offsets` (int32 [groups + 1], kept, not copied).  elems holds two codes a byte, row after
+    row; scales the blocks' scale bytes in the tensor core's order.  `stacked`: made from a tensor
+    of three dimensions [groups, rows / groups, cols].  `glu`: gate and linear rows interleaved by
+    mx4_quant_w13."""
+
+    __slots__ = ("elems", "scales", "rows", "cols", "groups", "offsets", "stacked", "glu")
+
+    def __init__(self, rows, cols, groups, offsets, stacked, device, glu=False):
+        e, s = c_size_t(0), c_size_t(0)
+        _check(lib().lmoe_mx4_bytes(rows, cols, groups, int(offsets is not None), ctypes.byref(e), ctypes.byref(s)),
+               "lmoe_mx4_bytes")
+        self.rows, self.cols, self.groups, self.offsets = rows, cols, groups, offsets
+        self.stacked, self.glu = stacked, glu
+        self.elems = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(s.value, dtype=torch.uint8, device=device)
+
+    def _match(self, rows, cols, groups, offsets, stacked, glu):
+        if (self.rows, self.cols, self.groups, self.stacked, self.glu) != (rows, cols, groups, stacked, glu) or \
+                (self.offsets is None) != (offsets is None):
+            raise LmoeError("out was made for a matrix of another shape")
+        self.offsets = offsets
+
+
+def mx4_quant(x, offsets=None, out=None, stream=None) -> Mx4:
+    """x in MXFP4: [rows, cols] (fp32 or bf16, cols a multiple of 32, any row stride), or stacked
+    matrices [groups, rows, cols].  offsets (int32 [groups + 1]): the rows' groups, for the grouped
+    product.  out: an Mx4 of an earlier call with the same shapes, to write into."""
+    dt = _dtype(x.dtype, "x")
+    if x.dim() not in (2, 3) or (x.dim() == 3 and offsets is not None):
+        raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets")
+    stacked = x.dim() == 3
+    groups = x.shape[0] if stacked else 1
+    if offsets is not None:
+        groups = _offsets(offsets).numel() - 1
+    if stacked:
+        if not x.is_contiguous():
+            raise LmoeError("stacked matrices must be contiguous")
+        rows, cols, ld = x.shape[0] * x.shape[1], x.shape[2], x.shape[2]
+    else:
+        rows, cols = x.shape
+        ld = x.stride(0) if rows > 1 else cols
+        if rows and ((cols > 1 and x.stride(1) != 1) or ld < cols):
+            raise LmoeError("x's columns must be contiguous and its rows must not overlap")
+    with _OnDevice(stream, x, offsets, *(() if out is None else (out.elems, out.scales))) as on:
+        if out is None:
+            out = Mx4(rows, cols, groups, offsets, stacked, x.device)
+        else:
+            out._match(rows, cols, groups, offsets, stacked, False)
+        _check(lib().lmoe_mx4_quant(_ptr(x), dt, ld, rows, cols, groups, _ptr(offsets), _ptr(out.elems),
+                                    _ptr(out.scales), _ptr(on.status), on.ptr), "lmoe_mx4_quant")
+    return out
+
+
+def mx4_quant_w13(w1, w3, out=None, stream=None) -> Mx4:
+    """A SwiGLU's gate and linear projections w1, w3 ([h, cols] or stacked [groups, h, cols], h a
+    multiple of 64) as one MXFP4 matrix for mx4_gemm(..., swiglu=True)."""
+    dt = _dtype(w1.dtype, "w1")
+    if w1.dim() not in (2, 3):
+        raise LmoeError("w1 must be [h, cols] or [groups, h, cols]")
+    _dev(w1, None, None, "w1")
+    _dev(w3, w1.dtype, w1.shape, "w3")
+    stacked = w1.dim() == 3
+    groups = w1.shape[0] if stacked else 1
+    h, cols = w1.shape[-2:]
+    with _OnDevice(stream, w1, w3, *(() if out is None else (out.elems, out.scales))) as on:
+        if out is None:
+            out = Mx4(2 * groups * h, cols, groups, None, stacked, w1.device, glu=True)
+        else:
+            out._match(2 * groups * h, cols, groups, None, stacked, True)
+        _check(lib().lmoe_mx4_quant_w13(_ptr(w1), _ptr(w3), dt, groups, h, cols, _ptr(out.elems), _ptr(out.scales),
+                                        _ptr(on.status), on.ptr), "lmoe_mx4_quant_w13")
+    return out
+
+
+def mx4_dequant(q: Mx4, dtype=torch.bfloat16, out=None, stream=None):
+    """The values q stands for, [rows, cols] (stacked matrices: [groups, rows / groups, cols]).
+    Rows of q that belong to no group: zeros, or left as they are in a given `out`."""
+    flags = 0
+    dt = _dtype(dtype if out is None else out.dtype, "dtype")
+    shape = (q.groups, q.rows // q.groups, q.cols) if q.stacked else (q.rows, q.cols)
+    with _OnDevice(stream, q.elems, q.scales, q.offsets, out) as on:
+        if out is None:
+            out, flags = torch.empty(shape, dtype=dtype, device=q.elems.device), MX4_ZERO_REST
+        if tuple(out.shape) != shape or not out.is_contiguous():
+            raise LmoeError(f"out must be contiguous and have shape {shape}")
+        _check(lib().lmoe_mx4_dequant(_ptr(q.elems), _ptr(q.scales), q.rows, q.cols, q.groups, _ptr(q.offsets),
+                                      _ptr(out), dt, q.cols, flags, _ptr(on.status), on.ptr), "lmoe_mx4_dequant")
+    return out
+
+
+def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, stream=None):
+    """a b^T of MXFP4 matrices with fp32 sums: [M, N] in fp32 or bf16.  b stacked [groups, N, K]: a
+    quantised with offsets, its rows of group g times matrix g.  swiglu=True: b from mx4_quant_w13,
+    the result bf16 silu(gate) * linear [M, N / 2].  Rows of a that belong to no group:
+    zeros, or left as they are in a given `out`."""
+    if a.stacked or a.glu:
+        raise LmoeError("a must be one matrix of rows")
+    if a.cols != b.cols:
+        raise LmoeError(f"a and b disagree on K ({a.cols} and {b.cols})")
+    if b.offsets is not None or (a.offsets is None) == b.stacked or a.groups != b.groups:
+        raise LmoeError("a product takes a plain matrix b, or a with offsets and as many stacked matrices b")
+    if bool(swiglu) != b.glu:
+        raise LmoeError("swiglu=True goes with a matrix from mx4_quant_w13")
+    M, N = a.rows, b.rows // b.groups
+    flags = MX4_SWIGLU if swiglu else 0
+    shape = (M, N // 2 if swiglu else N)
+    dt = _dtype(dtype if out is None else out.dtype, "dtype")
+    with _OnDevice(stream, a.elems, a.scales, a.offsets, b.elems, b.scales, out) as on:
+        if out is None:
+            out, flags = torch.empty(shape, dtype=dtype, device=a.elems.device), flags | MX4_ZERO_REST
+        elif tuple(out.shape) != shape or (shape[1] > 1 and out.stride(1) != 1) or \
+                (M > 1 and out.stride(0) < shape[1]):
+            raise LmoeError(f"out must have shape {shape}, contiguous columns and rows that do not overlap")
+        ld = out.stride(0) if M > 1 else shape[1]
+        _check(lib().lmoe_mx4_gemm(_ptr(a.elems), _ptr(a.scales), _ptr(b.elems), _ptr(b.scales), M, N, a.cols,
+                                   a.groups, _ptr(a.offsets), _ptr(out), dt, ld, flags, _ptr(on.status), on.ptr),
+               "lmoe_mx4_gemm")
+    return out
+
+
+_balance_scratch = None
+
+
+def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream=None):
+    """Balance loss of a router (lmoe_balance_loss): scores [T, E] fp32 and the choice idx [T, k] int32,
+    as Layer.routing() gives them; cu_seqlens (int32 [S + 1]) bounds the sequences (None: one).
+    Returns dict(loss [1] fp32, counts [S, E] int32, dscores [T, E] fp32): the gradient of the loss
+    in the scores, left out with grad=False.  `out` may pass preallocated buffers."""
+    global _balance_scratch
+    if scores.dim() != 2 or idx.dim() != 2:
+        raise LmoeError("scores must be [T, E] and idx [T, k]")
+    T, E = scores.shape
+    _dev(scores, torch.float32, (T, E), "scores")
+    k = idx.shape[1]
+    _dev(idx, torch.int32, (T, k), "idx")
+    S = 1
+    if cu_seqlens is not None:
+        _dev(_offsets(cu_seqlens), name="cu_seqlens")
+        S = cu_seqlens.numel() - 1
+    shapes = dict(loss=((1,), torch.float32), counts=((S, E), torch.int32))
+    if grad:
+        shapes["dscores"] = ((T, E), torch.float32)
+    out = dict(out or {})
+    for n in shapes.keys() & out.keys():
+        _dev(out[n], shapes[n][1], shapes[n][0], n)
+    if _balance_scratch is None:
+        n = c_size_t(0)
+        _check(lib().lmoe_balance_scratch_bytes(ctypes.byref(n)), "lmoe_balance_scratch_bytes")
+        _balance_scratch = n.value
+    with _OnDevice(stream, scores, idx, cu_seqlens, *(out[n] for n in shapes.keys() & out.keys())) as on:
+        for n, (shp, dt) in shapes.items():
+            if n not in out:
+                out[n] = torch.empty(shp, dtype=dt, device=scores.device)
+        scratch = torch.empty(_balance_scratch, dtype=torch.uint8, device=scores.device)
+        _check(lib().lmoe_balance_loss(_ptr(scores), _ptr(idx), T, E, k, _ptr(cu_seqlens), S, float(coef),
+                                       _ptr(out["counts"]), _ptr(out["loss"]),
+                                       _ptr(out["dscores"]) if grad else None, _ptr(scratch), _ptr(on.status),
+                                       on.ptr), "lmoe_balance_loss")
     return out
 
 

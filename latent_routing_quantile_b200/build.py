@@ -13,8 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblmoe.so")
-SOURCES = ["lmoe.cu"]
-HEADERS = ["bwd.cuh", "common.cuh", "host.cuh", "k1_router.cuh", "q8_gemm.cuh", "route.cuh", "tc_gemm.cuh"]
+SOURCES = ["lmoe.cu", "ops.cu"]
+HEADERS = ["balance.cuh", "bwd.cuh", "common.cuh", "host.cuh", "k1_router.cuh", "mx4.cuh", "mx4_gemm.cuh", "q8_gemm.cuh", "route.cuh", "tc_gemm.cuh"]
 
 
 def nvcc() -> str:
@@ -36,7 +36,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return LIB
     cmd = [nvcc(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-           "-Xcompiler", "-fPIC", "-shared", "-o", LIB + ".tmp",
+           "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-o", LIB + ".tmp",
            *[os.path.join(CSRC, s) for s in SOURCES], "-I", os.path.join(ROOT, "include")]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -1,0 +1,326 @@
+// Microscaled 4-bit floating point (MXFP4): quantisation, its inverse, and products on
+// tcgen05.mma.kind::mxf4 for sm_100a.
+//
+// Format: 32 consecutive values along K share a scale 2^X, X = floor(log2 max|v|) - 2 clamped to
+// [-127, 127] (-127 for a zero block), stored as the UE8M0 byte X + 127; a value is the E2M1 code of
+// v 2^-X (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign bit; nearest, ties to the even code, saturating at
+// 6), two codes to a byte, the first in the low half.  A block that holds a NaN or an infinity has
+// no such scale: its byte is 255 (UE8M0's NaN), and it stands for NaNs.
+//
+// Elements are row-major, cols / 2 bytes a row.  Scales are stored as the tensor core reads them:
+// the scales of 128 rows and 128 columns (4 blocks) form a 512-byte atom, byte 16 i + 4 j + b = row
+// i + 32 j, block b (i < 32, j < 4, b < 4), which one tcgen05.cp copies into four TMEM columns.
+// Atoms are stored row tile by row tile, two per 256 columns (one k-block of the products).  Blocks
+// past the last column have scale byte 0: their elements read as zeros, and 0 times a finite scale
+// adds nothing.  Rows come in groups (one for a plain matrix, an expert's rows, an expert's weight
+// matrix), and every group's atoms start with a tile of their own, so a tile of 128 rows never mixes
+// the scales of two groups, wherever the groups begin in the elements.
+#pragma once
+
+#include <cuda_fp4.h>
+
+#include "common.cuh"
+
+namespace lmoe {
+
+constexpr int kMx4MaxGroups = 1024;
+
+__host__ __device__ __forceinline__ int mx4_kblocks(int cols) { return (cols + 255) / 256; }
+
+// How the rows of a matrix fall into groups.
+struct Mx4Rows {
+  const int* offsets;  // device, [groups + 1]: first row of each group and the end; null: equal groups
+  int groups;
+  int rows;            // of the whole matrix
+};
+
+// Tiles of 128 rows, group by group.  Ragged groups need a prefix sum over the groups, which each
+// block makes once in shared memory.
+struct Mx4Tiles {
+  const int* first_tile;  // shared, [groups + 1] (ragged groups)
+  const int* first_row;   // shared, [groups + 1]
+  int groups, group_rows, tiles_per_group, total;
+  int rest_lo, rest_hi;   // rows [0, rest_lo) and [rest_hi, rows) belong to no group
+
+  // Group, first row and valid rows of tile t.
+  __device__ __forceinline__ void get(int t, int& g, int& row0, int& valid) const {
+    if (first_tile) {
+      int lo = 0, hi = groups;  // first_tile[lo] <= t < first_tile[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_tile[mid] <= t) lo = mid; else hi = mid;
+      }
+      g = lo;
+      const int within = (t - first_tile[g]) * 128;
+      row0 = first_row[g] + within;
+      valid = min(128, first_row[g + 1] - row0);
+    } else {
+      g = t / tiles_per_group;
+      const int within = (t - g * tiles_per_group) * 128;
+      row0 = g * group_rows + within;
+      valid = min(128, group_rows - within);
+    }
+  }
+};
+
+constexpr int kMx4TableInts = 2 * (kMx4MaxGroups + 1) + 2 + 32;
+
+// Fills the tile table (every thread of the block takes part; ends with a barrier).  Offsets that
+// decrease or leave [0, rows] are recorded as LMOE_STATUS_BAD_INDEX and give no tiles at all, so no
+// access follows from them (every row then belongs to no group).
+__device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* status) {
+  Mx4Tiles t;
+  t.groups = r.groups;
+  if (!r.offsets) {
+    t.first_tile = t.first_row = nullptr;
+    t.group_rows = r.rows / r.groups;
+    t.tiles_per_group = (t.group_rows + 127) >> 7;
+    t.total = t.tiles_per_group * r.groups;
+    t.rest_lo = 0;
+    t.rest_hi = r.rows;
+    return t;
+  }
+  int* first_tile = table;
+  int* first_row = table + kMx4MaxGroups + 1;
+  int* bad = table + 2 * (kMx4MaxGroups + 1);
+  int* wsum = bad + 2;
+  const int n = r.groups, tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    *bad = 0;
+    first_tile[0] = 0;
+  }
+  __syncthreads();
+  for (int g = tid; g <= n; g += nthr) {
+    const int v = r.offsets[g];
+    if (v < 0 || v > r.rows || (g && v < r.offsets[g - 1])) *bad = 1;
+    first_row[g] = v;
+  }
+  __syncthreads();
+  int base = 0;
+  for (int g0 = 0; g0 < n; g0 += nthr) {  // running sum of the groups' tiles, a block's width at a time
+    const int g = g0 + tid;
+    int v = g < n ? (first_row[g + 1] - first_row[g] + 127) >> 7 : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < (nthr >> 5); ++w) {
+      if (w < warp) before += wsum[w];
+      base += wsum[w];
+    }
+    if (g < n) first_tile[g + 1] = before + v;
+    __syncthreads();
+  }
+  t.first_tile = first_tile;
+  t.first_row = first_row;
+  t.group_rows = t.tiles_per_group = 0;
+  t.total = *bad ? 0 : base;
+  t.rest_lo = *bad ? r.rows : first_row[0];
+  t.rest_hi = *bad ? r.rows : first_row[n];
+  if (*bad && tid == 0) set_status(status, LMOE_STATUS_BAD_INDEX);
+  return t;
+}
+
+// Zeroes row i of the rows that belong to no group, for i = first, first + stride, ... (a warp a row).
+template <typename T>
+__device__ __forceinline__ void mx4_zero_rest(const Mx4Tiles& t, int rows, T* out, long long ld, int cols, int first,
+                                              int stride, int lane) {
+  const int n = t.rest_lo + rows - t.rest_hi;
+  for (int i = first; i < n; i += stride) {
+    T* row = out + (long long)(i < t.rest_lo ? i : t.rest_hi + i - t.rest_lo) * ld;
+    for (int c = lane; c < cols; c += 32) row[c] = from_f<T>(0.f);
+  }
+}
+
+// --------------------------------------------------------------------------- quantisation
+// Scale byte of a block whose largest magnitude has the fp32 bits `amax` (NaN and infinity compare
+// above every number): the exponent field less 2, so that the largest value lands in [4, 8).
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax) {
+  const int e = (int)(amax >> 23);
+  return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+}
+
+// Eight values, scaled, as eight codes (the first in the lowest four bits).
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float s) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * j] * s, v[2 * j + 1] * s), __NV_E2M1, cudaRoundNearest)
+         << (8 * j);
+  return w;
+}
+
+// Eight values of a row as fp32; `vec`: the row starts on a 16-byte boundary.
+__device__ __forceinline__ void mx4_load8(const bf16* p, bool vec, float (&v)[8]) {
+  if (vec) {
+    const uint4 q = ldg_nc_v4(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = bf2f(p[j]);
+  }
+}
+__device__ __forceinline__ void mx4_load8(const float* p, bool vec, float (&v)[8]) {
+  if (vec) {
+    const uint4 a = ldg_nc_v4(p), b = ldg_nc_v4(p + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[j];
+  }
+}
+
+struct Mx4QuantParams {
+  const void* src;   // [rows, ld]; PAIRED: w1 [groups, h, cols]
+  const void* src3;  // PAIRED: w3
+  long long ld;
+  int cols;
+  Mx4Rows rows;
+  uint8_t* elems;
+  uint8_t* scales;
+  uint32_t* status;
+  int vec;           // every row of src starts on a 16-byte boundary
+};
+
+// A block takes one tile of 128 rows and 256 columns at a time (a grid of persistent blocks walks
+// them); a lane takes 8 of a row's 32-value blocks' values, four lanes a block, so a warp reads a
+// row's 256 values at once and writes their codes as one 128-byte line.  The tile's scale bytes
+// gather in shared memory in atom order and leave as two whole atoms.
+// PAIRED: rows are the gate and linear projections of a SwiGLU interleaved in groups of 64 (row
+// 128 (j / 64) + j % 64 = w1[j], 64 further w3[j]).
+template <typename T, bool PAIRED>
+__global__ void __launch_bounds__(256) mx4_quant_kernel(const Mx4QuantParams p) {
+  __shared__ int table[kMx4TableInts];
+  __shared__ __align__(16) uint8_t sf[1024];
+  pdl_wait();
+  pdl_trigger();
+  const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkb = mx4_kblocks(p.cols);
+  const long long n = (long long)tiles.total * nkb;
+  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
+    const int t = (int)(u / nkb), kb = (int)(u - (long long)t * nkb);
+    int g, row0, valid;
+    tiles.get(t, g, row0, valid);
+    if (threadIdx.x < 64) reinterpret_cast<uint4*>(sf)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const int c = kb * 256 + lane * 8;
+    const bool in = c < p.cols;  // cols is a multiple of 32: a block is inside or outside whole
+#pragma unroll 4
+    for (int r = warp; r < valid; r += 8) {
+      float v[8];
+      const int row = row0 + r;
+      if (in) {
+        if constexpr (PAIRED) {
+          // row of the interleaved matrix -> row of w1 or w3 (group g has 2h rows)
+          const int within = row - g * tiles.group_rows;
+          const long long srow = (long long)g * (tiles.group_rows >> 1) + (within >> 7) * 64 + (within & 63);
+          mx4_load8(static_cast<const T*>((within & 64) ? p.src3 : p.src) + srow * p.ld + c, p.vec, v);
+        } else {
+          mx4_load8(static_cast<const T*>(p.src) + (long long)row * p.ld + c, p.vec, v);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      }
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const uint32_t sb = mx4_scale_byte(amax);
+      // 2^-X = 2^(127 - byte): exponent field 254 - byte, at least 2 for every finite block
+      const float s = __uint_as_float((254u - min(sb, 252u)) << 23);
+      if (in) {
+        *reinterpret_cast<uint32_t*>(p.elems + (long long)row * (p.cols >> 1) + (c >> 1)) = e2m1x8(v, s);
+        if ((lane & 3) == 0)
+          sf[(lane >> 4) * 512 + 16 * (r & 31) + 4 * (r >> 5) + ((lane >> 2) & 3)] = (uint8_t)sb;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 64)
+      reinterpret_cast<uint4*>(p.scales + u * 1024)[threadIdx.x] = reinterpret_cast<uint4*>(sf)[threadIdx.x];
+    __syncthreads();
+  }
+}
+
+// --------------------------------------------------------------------------- dequantisation
+struct Mx4DequantParams {
+  const uint8_t* elems;
+  const uint8_t* scales;
+  void* out;         // [rows, ld]
+  long long ld;
+  int cols;
+  Mx4Rows rows;
+  uint32_t* status;
+  int vec;
+  int zero_rest;     // 1: rows of no group are set to zero
+};
+
+// The value of code c (4 bits) times 2^X.  E2M1 is widened to fp32 by its bits: exponent field e, one
+// mantissa bit m: e > 0: (1 + m/2) 2^(e-1); e = 0: m/2.
+__device__ __forceinline__ float e2m1_value(uint32_t c, float s) {
+  const uint32_t m = c & 7u;
+  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float((((m >> 1) + 126u) << 23) | ((m & 1u) << 22));
+  return ((c & 8u) ? -a : a) * s;
+}
+
+// Same tiles and lanes as the quantisation.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dequant_kernel(const Mx4DequantParams p) {
+  __shared__ int table[kMx4TableInts];
+  pdl_wait();
+  pdl_trigger();
+  const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkb = mx4_kblocks(p.cols);
+  const long long n = (long long)tiles.total * nkb;
+  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
+    const int t = (int)(u / nkb), kb = (int)(u - (long long)t * nkb);
+    int g, row0, valid;
+    tiles.get(t, g, row0, valid);
+    const int c = kb * 256 + lane * 8;
+    if (c >= p.cols) continue;
+    const uint8_t* sf = p.scales + u * 1024 + (lane >> 4) * 512 + ((lane >> 2) & 3);
+#pragma unroll 4
+    for (int r = warp; r < valid; r += 8) {
+      const long long row = row0 + r;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(p.elems + row * (p.cols >> 1) + (c >> 1));
+      const uint32_t sb = sf[16 * (r & 31) + 4 * (r >> 5)];
+      // 2^(byte - 127): a subnormal for byte 0, NaN for 255
+      const float s = sb == 255u ? __uint_as_float(0x7FC00000u)
+                                 : (sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u));
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = e2m1_value(w >> (4 * j), s);
+      T* o = static_cast<T*>(p.out) + row * p.ld + c;
+      if (p.vec) {
+        if constexpr (sizeof(T) == 4) {
+          reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = from_f<T>(v[j]);
+      }
+    }
+  }
+  if (p.zero_rest)
+    mx4_zero_rest(tiles, p.rows.rows, static_cast<T*>(p.out), p.ld, p.cols, blockIdx.x * 8 + warp, gridDim.x * 8, lane);
+}
+
+}  // namespace lmoe

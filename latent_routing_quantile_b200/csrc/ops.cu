@@ -1,0 +1,268 @@
+// Host side of the entry points that need no layer handle and work on the caller's buffers: MXFP4
+// quantisation, dequantisation and products, and the router's balance loss.
+#include <algorithm>
+#include <cstring>
+
+#include "balance.cuh"
+#include "host.cuh"
+#include "mx4_gemm.cuh"
+
+using namespace lmoe;
+
+namespace {
+
+int device_sms(int* sms) {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LMOE_ECUDA;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return LMOE_ECUDA;
+  return major == 10 ? LMOE_OK : LMOE_EDEVICE;
+}
+
+// Sizes of a matrix in groups: rows and 128-row tiles stay within 32-bit indices.
+int check_rows(int64_t rows, int32_t cols, int32_t groups, bool ragged) {
+  if (rows < 0 || cols <= 0 || groups <= 0) return LMOE_EINVAL;
+  if (!ragged && rows % groups) return LMOE_EINVAL;
+  if (cols % 32 || groups > kMx4MaxGroups || rows > (1ll << 30)) return LMOE_EUNSUPPORTED;
+  return LMOE_OK;
+}
+long long scale_tiles(int64_t rows, int32_t groups, bool ragged) {
+  return ragged ? (rows + 127) / 128 + groups : (rows / groups + 127) / 128 * groups;
+}
+
+template <typename T>
+bool rows16(const void* p, int64_t ld) {
+  return ((uintptr_t)p & 15) == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+}
+
+// Persistent grid of the quantisation kernels: four blocks of 256 threads an SM.
+int mx4_grid(long long tiles, int nkb, int sms) {
+  const long long n = tiles * nkb;
+  return (int)(n < 4ll * sms ? (n < 1 ? 1 : n) : 4ll * sms);
+}
+
+}  // namespace
+
+extern "C" {
+
+int lmoe_mx4_bytes(int64_t rows, int32_t cols, int32_t groups, int32_t ragged, size_t* elem_bytes,
+                   size_t* scale_bytes) {
+  const int rc = check_rows(rows, cols, groups, ragged != 0);
+  if (rc) return rc;
+  if (!elem_bytes || !scale_bytes) return LMOE_EINVAL;
+  *elem_bytes = (size_t)rows * (cols / 2);
+  *scale_bytes = (size_t)scale_tiles(rows, groups, ragged != 0) * mx4_kblocks(cols) * 1024;
+  return LMOE_OK;
+}
+
+int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t cols, int32_t groups,
+                   const int32_t* offsets, uint8_t* elems, uint8_t* scales, uint32_t* status, void* stream) {
+  const int rc = check_rows(rows, cols, groups, offsets != nullptr);
+  if (rc) return rc;
+  if (dtype != LMOE_F32 && dtype != LMOE_BF16) return LMOE_EINVAL;
+  if (rows == 0) return LMOE_OK;
+  if (!x || !elems || !scales || !status || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
+    return LMOE_EINVAL;
+  if ((uintptr_t)x % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
+  int sms = 0;
+  const int drc = device_sms(&sms);
+  if (drc) return drc;
+  Mx4QuantParams p;
+  memset(&p, 0, sizeof(p));
+  p.src = x;
+  p.ld = ld;
+  p.cols = cols;
+  p.rows = Mx4Rows{offsets, groups, (int)rows};
+  p.elems = elems;
+  p.scales = scales;
+  p.status = status;
+  p.vec = dtype == LMOE_F32 ? rows16<float>(x, ld) : rows16<bf16>(x, ld);
+  const int grid = mx4_grid(scale_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == LMOE_F32)
+    CK(launch_k(mx4_quant_kernel<float, false>, dim3(grid), dim3(256), 0, st, 1, p));
+  else
+    CK(launch_k(mx4_quant_kernel<bf16, false>, dim3(grid), dim3(256), 0, st, 1, p));
+  return LMOE_OK;
+}
+
+int lmoe_mx4_quant_w13(const void* w1, const void* w3, int32_t dtype, int32_t groups, int32_t h, int32_t cols,
+                       uint8_t* elems, uint8_t* scales, uint32_t* status, void* stream) {
+  if (h <= 0 || groups <= 0) return LMOE_EINVAL;
+  if (h % 64) return LMOE_EUNSUPPORTED;
+  const int64_t rows = 2ll * groups * h;
+  const int rc = check_rows(rows, cols, groups, false);
+  if (rc) return rc;
+  if (dtype != LMOE_F32 && dtype != LMOE_BF16) return LMOE_EINVAL;
+  if (!w1 || !w3 || !elems || !scales || !status || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
+    return LMOE_EINVAL;
+  if (((uintptr_t)w1 | (uintptr_t)w3) % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
+  int sms = 0;
+  const int drc = device_sms(&sms);
+  if (drc) return drc;
+  Mx4QuantParams p;
+  memset(&p, 0, sizeof(p));
+  p.src = w1;
+  p.src3 = w3;
+  p.ld = cols;
+  p.cols = cols;
+  p.rows = Mx4Rows{nullptr, groups, (int)rows};
+  p.elems = elems;
+  p.scales = scales;
+  p.status = status;
+  p.vec = (((uintptr_t)w1 | (uintptr_t)w3) & 15) == 0;  // cols is a multiple of 32
+  const int grid = mx4_grid(scale_tiles(rows, groups, false), mx4_kblocks(cols), sms);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == LMOE_F32)
+    CK(launch_k(mx4_quant_kernel<float, true>, dim3(grid), dim3(256), 0, st, 1, p));
+  else
+    CK(launch_k(mx4_quant_kernel<bf16, true>, dim3(grid), dim3(256), 0, st, 1, p));
+  return LMOE_OK;
+}
+
+int lmoe_mx4_dequant(const uint8_t* elems, const uint8_t* scales, int64_t rows, int32_t cols, int32_t groups,
+                     const int32_t* offsets, void* out, int32_t dtype, int64_t ld, uint32_t flags, uint32_t* status,
+                     void* stream) {
+  const int rc = check_rows(rows, cols, groups, offsets != nullptr);
+  if (rc) return rc;
+  if ((dtype != LMOE_F32 && dtype != LMOE_BF16) || (flags & ~LMOE_MX4_ZERO_REST)) return LMOE_EINVAL;
+  if (rows == 0) return LMOE_OK;
+  if (!out || !elems || !scales || !status || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
+    return LMOE_EINVAL;
+  if ((uintptr_t)out % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
+  int sms = 0;
+  const int drc = device_sms(&sms);
+  if (drc) return drc;
+  Mx4DequantParams p;
+  memset(&p, 0, sizeof(p));
+  p.elems = elems;
+  p.scales = scales;
+  p.out = out;
+  p.ld = ld;
+  p.cols = cols;
+  p.rows = Mx4Rows{offsets, groups, (int)rows};
+  p.status = status;
+  p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
+  p.vec = dtype == LMOE_F32 ? rows16<float>(out, ld) : rows16<bf16>(out, ld);
+  const int grid = mx4_grid(scale_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == LMOE_F32)
+    CK(launch_k(mx4_dequant_kernel<float>, dim3(grid), dim3(256), 0, st, 1, p));
+  else
+    CK(launch_k(mx4_dequant_kernel<bf16>, dim3(grid), dim3(256), 0, st, 1, p));
+  return LMOE_OK;
+}
+
+int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t* b_elems, const uint8_t* b_scales,
+                  int32_t M, int32_t N, int32_t K, int32_t groups, const int32_t* offsets, void* c, int32_t c_dtype,
+                  int64_t ldc, uint32_t flags, uint32_t* status, void* stream) {
+  if (M < 0 || N <= 0 || K <= 0 || groups <= 0) return LMOE_EINVAL;
+  if ((groups > 1 && !offsets) || (flags & ~(LMOE_MX4_SWIGLU | LMOE_MX4_ZERO_REST))) return LMOE_EINVAL;
+  const bool swiglu = (flags & LMOE_MX4_SWIGLU) != 0;
+  if (c_dtype != LMOE_F32 && c_dtype != LMOE_BF16) return LMOE_EINVAL;
+  int rc = check_rows(M, K, groups, offsets != nullptr);
+  if (!rc) rc = check_rows((int64_t)groups * N, K, groups, false);
+  if (rc) return rc;
+  if (swiglu && (N % 128 || c_dtype != LMOE_BF16)) return LMOE_EUNSUPPORTED;
+  if (M == 0) return LMOE_OK;
+  const int32_t cols = swiglu ? N / 2 : N;
+  if (!a_elems || !a_scales || !b_elems || !b_scales || !c || !status || ldc < cols) return LMOE_EINVAL;
+  if (((uintptr_t)a_elems | (uintptr_t)a_scales | (uintptr_t)b_elems | (uintptr_t)b_scales) & 15) return LMOE_EINVAL;
+  if ((uintptr_t)c % (c_dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  Mx4GemmParams p;
+  memset(&p, 0, sizeof(p));
+  if (!make_map_u8(&p.tmA, a_elems, M, K / 2, K / 2, 128) ||
+      !make_map_u8(&p.tmB, b_elems, (long long)groups * N, K / 2, K / 2, 128))
+    return LMOE_ECUDA;
+  p.a_sf = a_scales;
+  p.b_sf = b_scales;
+  p.rows = Mx4Rows{offsets, groups, M};
+  p.N = N;
+  p.n_tiles = (N + 127) / 128;
+  p.nkb = mx4_kblocks(K);
+  p.c = c;
+  p.ldc = ldc;
+  p.c_cols = cols;
+  p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
+  p.vec = c_dtype == LMOE_F32 ? rows16<float>(c, ldc) : rows16<bf16>(c, ldc);
+  p.status = status;
+  const long long tiles = scale_tiles(M, groups, offsets != nullptr) * p.n_tiles;
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  cudaStream_t st = (cudaStream_t)stream;
+  auto run = [&](auto kern, unsigned& done) -> int {
+    CK(ensure_smem_attr(kern, kMx4SmemBytes, done));
+    CK(launch_k(kern, dim3(grid), dim3(kMx4Threads), kMx4SmemBytes, st, 1, p));
+    return LMOE_OK;
+  };
+  static unsigned done[3] = {0, 0, 0};
+  if (swiglu) return run(mx4_gemm_kernel<bf16, true>, done[0]);
+  if (c_dtype == LMOE_BF16) return run(mx4_gemm_kernel<bf16, false>, done[1]);
+  return run(mx4_gemm_kernel<float, false>, done[2]);
+}
+
+int lmoe_balance_scratch_bytes(size_t* bytes) {
+  if (!bytes) return LMOE_EINVAL;
+  *bytes = kBalMaxBlocks * sizeof(double) + 256;
+  return LMOE_OK;
+}
+
+int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_t E, int32_t k,
+                      const int32_t* cu_seqlens, int32_t S, float coef, int32_t* counts, float* loss, float* dscores,
+                      void* scratch, uint32_t* status, void* stream) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E || S <= 0 || (!cu_seqlens && S != 1) || !(coef == coef)) return LMOE_EINVAL;
+  if (E > 1024 || k > 32 || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
+  if (!counts || !loss || !scratch || !status || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
+  if (T && (!scores || !idx)) return LMOE_EINVAL;
+  if (((uintptr_t)scores | (uintptr_t)dscores | (uintptr_t)idx | (uintptr_t)counts | (uintptr_t)loss) & 3)
+    return LMOE_EINVAL;
+  int sms = 0;
+  const int rc = device_sms(&sms);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  CK(cudaMemsetAsync(counts, 0, (size_t)S * E * sizeof(int32_t), st));
+  if (T == 0) {
+    CK(cudaMemsetAsync(loss, 0, sizeof(float), st));
+    return LMOE_OK;
+  }
+  BalanceParams p;
+  memset(&p, 0, sizeof(p));
+  p.scores = scores;
+  p.idx = idx;
+  p.cu = cu_seqlens;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.S = S;
+  p.coef = coef;
+  p.counts = counts;
+  p.loss = loss;
+  p.dscores = dscores;
+  p.done = static_cast<unsigned*>(scratch);
+  p.partial = reinterpret_cast<double*>(static_cast<char*>(scratch) + 256);
+  p.status = status;
+  // counting: runs of at least 256 tokens, two blocks an SM
+  p.chunk = std::max(256, (T + 2 * sms - 1) / (2 * sms));
+  CK(launch_k(balance_count_kernel, dim3((T + p.chunk - 1) / p.chunk), dim3(kBalThreads), E * sizeof(int), st, 1, p));
+  // the pass over the scores: at least a token a warp, at most eight blocks an SM
+  const int blocks = std::min(8 * sms, kBalMaxBlocks);
+  p.chunk = std::max(8, (T + blocks - 1) / blocks);
+  const dim3 grid((T + p.chunk - 1) / p.chunk), block(kBalThreads);
+  const bool vec = E % 4 == 0 && (((uintptr_t)scores | (uintptr_t)dscores) & 15) == 0;
+  if (vec) {
+    if (E <= 128) CK(launch_k(balance_kernel<1, 4>, grid, block, 0, st, 1, p));
+    else if (E <= 256) CK(launch_k(balance_kernel<2, 4>, grid, block, 0, st, 1, p));
+    else if (E <= 512) CK(launch_k(balance_kernel<4, 4>, grid, block, 0, st, 1, p));
+    else CK(launch_k(balance_kernel<8, 4>, grid, block, 0, st, 1, p));
+  } else {
+    if (E <= 64) CK(launch_k(balance_kernel<2, 1>, grid, block, 0, st, 1, p));
+    else if (E <= 256) CK(launch_k(balance_kernel<8, 1>, grid, block, 0, st, 1, p));
+    else CK(launch_k(balance_kernel<32, 1>, grid, block, 0, st, 1, p));
+  }
+  return LMOE_OK;
+}
+
+}  // extern "C"
