@@ -458,87 +458,89 @@ def route_noalloc(scores, bias, k, out=None, stream=None):
 
 
 # --------------------------------------------------------------------------- operators on the caller's tensors
-_status_words = {}
+# Small calls last a few microseconds on the GPU, so their host side is kept short: plain integers to
+# ctypes, sizes worked out here, one look at the current device and stream.
+_status_words = {}  # device index -> (tensor, address)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _status_word(dev):
-    """The device word that the operators below OR their fault bits into (one a device)."""
-    if dev not in _status_words:
+def _status_word(index: int) -> int:
+    """Address of the device word that the operators below OR their fault bits into (one a device)."""
+    w = _status_words.get(index)
+    if w is None:
         if torch.cuda.is_current_stream_capturing():
             raise LmoeError("the first operator call on a device cannot be captured: make one before the capture")
-        _status_words[dev] = torch.zeros(1, dtype=torch.int32, device=dev)
-        torch.cuda.synchronize(dev)
-    return _status_words[dev]
+        word = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
+        torch.cuda.synchronize(index)
+        w = _status_words[index] = (word, word.data_ptr())
+    return w[1]
 
 
 def op_status(device=None) -> int:
     """Fault bits (STATUS_*) of the mx4_* and balance_loss calls on `device` since the last read;
     synchronises the device and clears them."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    if dev not in _status_words:
+    index = None if device is None else torch.device(device).index
+    index = torch.cuda.current_device() if index is None else index
+    if index not in _status_words:
         return 0
-    torch.cuda.synchronize(dev)
-    v = int(_status_words[dev].item()) & 0xffffffff
-    _status_words[dev].zero_()
-    torch.cuda.synchronize(dev)
+    word = _status_words[index][0]
+    torch.cuda.synchronize(index)
+    v = int(word.item()) & 0xffffffff
+    word.zero_()
+    torch.cuda.synchronize(index)
     return v
 
 
-class _OnDevice:
-    """Runs an operator on the device of its tensors: makes that device and the call's stream
-    current (new tensors then belong to that stream), and tells torch that the tensors are in use
-    there when the caller names a stream of its own."""
+def _device_of(*tensors) -> int:
+    """The one CUDA device of the tensors (None entries are skipped)."""
+    index = tensors[0].get_device()
+    if index < 0:
+        raise LmoeError("tensors must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise LmoeError(f"tensors on different devices ({tensors[0].device} and {t.device})")
+    return index
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        if dev.type != "cuda":
-            raise LmoeError("tensors must be CUDA tensors")
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise LmoeError(f"tensors on different devices ({dev} and {t.device})")
-        if stream is not None and stream.device != dev:
-            raise LmoeError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.dev, self.named = dev, stream is not None
-        self.stream = stream if self.named else torch.cuda.current_stream(dev)
+
+class _Elsewhere:
+    """The rare form of an operator call, on a stream the caller names or on a device that is not the
+    current one: makes the device and stream current around the call (new tensors then belong to
+    that stream) and tells torch which tensors are in use there."""
+
+    def __init__(self, index, stream, *tensors):
+        if stream is not None and stream.device.index != index:
+            raise LmoeError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        self.named = stream is not None
+        self.stream = stream if self.named else torch.cuda.current_stream(index)
         self.tensors = tensors
-        self.ctx = None
-        if self.named or torch.cuda.current_device() != dev.index:
-            self.ctx = torch.cuda.stream(self.stream)
+        self.ctx = torch.cuda.stream(self.stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.status = _status_word(self.dev)
-        return self
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
         if self.named:
             for t in self.tensors:
                 if t is not None:
                     t.record_stream(self.stream)
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
         return False
-
-    @property
-    def ptr(self):
-        return c_void_p(self.stream.cuda_stream)
 
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _dtype(dtype, name):
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise LmoeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
-    return _DTYPES[dtype]
+    return dt
 
 
-def _offsets(offsets):
+def _offsets(offsets, name="offsets"):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
-        raise LmoeError("offsets must be a contiguous int32 tensor of one dimension, groups + 1 long")
+        raise LmoeError(f"{name} must be a contiguous int32 tensor of one dimension and at least two entries")
     return offsets
 
 
@@ -552,13 +554,14 @@ class Mx4:
     __slots__ = ("elems", "scales", "rows", "cols", "groups", "offsets", "stacked", "glu")
 
     def __init__(self, rows, cols, groups, offsets, stacked, device, glu=False):
-        e, s = c_size_t(0), c_size_t(0)
-        _check(lib().lmoe_mx4_bytes(rows, cols, groups, int(offsets is not None), ctypes.byref(e), ctypes.byref(s)),
-               "lmoe_mx4_bytes")
+        if cols % 32 or cols == 0:
+            raise LmoeError(f"columns must be a positive multiple of 32, got {cols}")
         self.rows, self.cols, self.groups, self.offsets = rows, cols, groups, offsets
         self.stacked, self.glu = stacked, glu
+        # the sizes of lmoe_mx4_bytes
+        tiles = (rows // groups + 127) // 128 * groups if offsets is None else (rows + 127) // 128 + groups
         self.elems = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
-        self.scales = torch.empty(s.value, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(tiles * ((cols + 255) // 256) * 1024, dtype=torch.uint8, device=device)
 
     def _match(self, rows, cols, groups, offsets, stacked, glu):
         if (self.rows, self.cols, self.groups, self.stacked, self.glu) != (rows, cols, groups, stacked, glu) or \
@@ -572,28 +575,38 @@ def mx4_quant(x, offsets=None, out=None, stream=None) -> Mx4:
     matrices [groups, rows, cols].  offsets (int32 [groups + 1]): the rows' groups, for the grouped
     product.  out: an Mx4 of an earlier call with the same shapes, to write into."""
     dt = _dtype(x.dtype, "x")
-    if x.dim() not in (2, 3) or (x.dim() == 3 and offsets is not None):
-        raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets")
-    stacked = x.dim() == 3
-    groups = x.shape[0] if stacked else 1
-    if offsets is not None:
-        groups = _offsets(offsets).numel() - 1
-    if stacked:
+    shape = x.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        groups, stacked = 1, False
+        ld, step = x.stride()
+        if rows <= 1:
+            ld = cols
+        if (step != 1 and rows and cols > 1) or ld < cols:
+            raise LmoeError("x's columns must be contiguous and its rows must not overlap")
+        if offsets is not None:
+            groups = _offsets(offsets).numel() - 1
+    elif len(shape) == 3 and offsets is None:
         if not x.is_contiguous():
             raise LmoeError("stacked matrices must be contiguous")
-        rows, cols, ld = x.shape[0] * x.shape[1], x.shape[2], x.shape[2]
+        groups, stacked = shape[0], True
+        if groups == 0:
+            raise LmoeError("x must hold at least one matrix")
+        rows, cols, ld = groups * shape[1], shape[2], shape[2]
     else:
-        rows, cols = x.shape
-        ld = x.stride(0) if rows > 1 else cols
-        if rows and ((cols > 1 and x.stride(1) != 1) or ld < cols):
-            raise LmoeError("x's columns must be contiguous and its rows must not overlap")
-    with _OnDevice(stream, x, offsets, *(() if out is None else (out.elems, out.scales))) as on:
-        if out is None:
-            out = Mx4(rows, cols, groups, offsets, stacked, x.device)
-        else:
-            out._match(rows, cols, groups, offsets, stacked, False)
-        _check(lib().lmoe_mx4_quant(_ptr(x), dt, ld, rows, cols, groups, _ptr(offsets), _ptr(out.elems),
-                                    _ptr(out.scales), _ptr(on.status), on.ptr), "lmoe_mx4_quant")
+        raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets")
+    kept = (x, offsets) if out is None else (x, offsets, out.elems, out.scales)
+    dev = _device_of(*kept)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _Elsewhere(dev, stream, *kept):
+            return mx4_quant(x, offsets, out)
+    if out is None:
+        out = Mx4(rows, cols, groups, offsets, stacked, x.device)
+    else:
+        out._match(rows, cols, groups, offsets, stacked, False)
+    _check(lib().lmoe_mx4_quant(x.data_ptr(), dt, ld, rows, cols, groups,
+                                None if offsets is None else offsets.data_ptr(), out.elems.data_ptr(),
+                                out.scales.data_ptr(), _status_word(dev), _raw_stream(dev)), "lmoe_mx4_quant")
     return out
 
 
@@ -601,44 +614,53 @@ def mx4_quant_w13(w1, w3, out=None, stream=None) -> Mx4:
     """A SwiGLU's gate and linear projections w1, w3 ([h, cols] or stacked [groups, h, cols], h a
     multiple of 64) as one MXFP4 matrix for mx4_gemm(..., swiglu=True)."""
     dt = _dtype(w1.dtype, "w1")
-    if w1.dim() not in (2, 3):
+    if w1.dim() not in (2, 3) or w1.numel() == 0:
         raise LmoeError("w1 must be [h, cols] or [groups, h, cols]")
     _dev(w1, None, None, "w1")
     _dev(w3, w1.dtype, w1.shape, "w3")
     stacked = w1.dim() == 3
     groups = w1.shape[0] if stacked else 1
     h, cols = w1.shape[-2:]
-    with _OnDevice(stream, w1, w3, *(() if out is None else (out.elems, out.scales))) as on:
-        if out is None:
-            out = Mx4(2 * groups * h, cols, groups, None, stacked, w1.device, glu=True)
-        else:
-            out._match(2 * groups * h, cols, groups, None, stacked, True)
-        _check(lib().lmoe_mx4_quant_w13(_ptr(w1), _ptr(w3), dt, groups, h, cols, _ptr(out.elems), _ptr(out.scales),
-                                        _ptr(on.status), on.ptr), "lmoe_mx4_quant_w13")
+    kept = (w1, w3) if out is None else (w1, w3, out.elems, out.scales)
+    dev = _device_of(*kept)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _Elsewhere(dev, stream, *kept):
+            return mx4_quant_w13(w1, w3, out)
+    if out is None:
+        out = Mx4(2 * groups * h, cols, groups, None, stacked, w1.device, glu=True)
+    else:
+        out._match(2 * groups * h, cols, groups, None, stacked, True)
+    _check(lib().lmoe_mx4_quant_w13(w1.data_ptr(), w3.data_ptr(), dt, groups, h, cols, out.elems.data_ptr(),
+                                    out.scales.data_ptr(), _status_word(dev), _raw_stream(dev)), "lmoe_mx4_quant_w13")
     return out
 
 
 def mx4_dequant(q: Mx4, dtype=torch.bfloat16, out=None, stream=None):
     """The values q stands for, [rows, cols] (stacked matrices: [groups, rows / groups, cols]).
     Rows of q that belong to no group: zeros, or left as they are in a given `out`."""
-    flags = 0
     dt = _dtype(dtype if out is None else out.dtype, "dtype")
     shape = (q.groups, q.rows // q.groups, q.cols) if q.stacked else (q.rows, q.cols)
-    with _OnDevice(stream, q.elems, q.scales, q.offsets, out) as on:
-        if out is None:
-            out, flags = torch.empty(shape, dtype=dtype, device=q.elems.device), MX4_ZERO_REST
-        if tuple(out.shape) != shape or not out.is_contiguous():
-            raise LmoeError(f"out must be contiguous and have shape {shape}")
-        _check(lib().lmoe_mx4_dequant(_ptr(q.elems), _ptr(q.scales), q.rows, q.cols, q.groups, _ptr(q.offsets),
-                                      _ptr(out), dt, q.cols, flags, _ptr(on.status), on.ptr), "lmoe_mx4_dequant")
+    if out is not None and (tuple(out.shape) != shape or not out.is_contiguous()):
+        raise LmoeError(f"out must be contiguous and have shape {shape}")
+    kept = (q.elems, q.scales, q.offsets, out)
+    dev = _device_of(*kept)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _Elsewhere(dev, stream, *kept):
+            return mx4_dequant(q, dtype, out)
+    flags = 0
+    if out is None:
+        out, flags = torch.empty(shape, dtype=dtype, device=q.elems.device), MX4_ZERO_REST
+    _check(lib().lmoe_mx4_dequant(q.elems.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, q.groups,
+                                  None if q.offsets is None else q.offsets.data_ptr(), out.data_ptr(), dt, q.cols,
+                                  flags, _status_word(dev), _raw_stream(dev)), "lmoe_mx4_dequant")
     return out
 
 
 def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, stream=None):
     """a b^T of MXFP4 matrices with fp32 sums: [M, N] in fp32 or bf16.  b stacked [groups, N, K]: a
     quantised with offsets, its rows of group g times matrix g.  swiglu=True: b from mx4_quant_w13,
-    the result bf16 silu(gate) * linear [M, N / 2].  Rows of a that belong to no group:
-    zeros, or left as they are in a given `out`."""
+    the result bf16 silu(gate) * linear [M, N / 2].  Rows of a that belong to no group: zeros, or
+    left as they are in a given `out`."""
     if a.stacked or a.glu:
         raise LmoeError("a must be one matrix of rows")
     if a.cols != b.cols:
@@ -648,23 +670,29 @@ def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, strea
     if bool(swiglu) != b.glu:
         raise LmoeError("swiglu=True goes with a matrix from mx4_quant_w13")
     M, N = a.rows, b.rows // b.groups
-    flags = MX4_SWIGLU if swiglu else 0
-    shape = (M, N // 2 if swiglu else N)
+    cols = N // 2 if swiglu else N
     dt = _dtype(dtype if out is None else out.dtype, "dtype")
-    with _OnDevice(stream, a.elems, a.scales, a.offsets, b.elems, b.scales, out) as on:
-        if out is None:
-            out, flags = torch.empty(shape, dtype=dtype, device=a.elems.device), flags | MX4_ZERO_REST
-        elif tuple(out.shape) != shape or (shape[1] > 1 and out.stride(1) != 1) or \
-                (M > 1 and out.stride(0) < shape[1]):
-            raise LmoeError(f"out must have shape {shape}, contiguous columns and rows that do not overlap")
-        ld = out.stride(0) if M > 1 else shape[1]
-        _check(lib().lmoe_mx4_gemm(_ptr(a.elems), _ptr(a.scales), _ptr(b.elems), _ptr(b.scales), M, N, a.cols,
-                                   a.groups, _ptr(a.offsets), _ptr(out), dt, ld, flags, _ptr(on.status), on.ptr),
-               "lmoe_mx4_gemm")
+    if out is not None and (tuple(out.shape) != (M, cols) or (cols > 1 and out.stride(1) != 1) or
+                            (M > 1 and out.stride(0) < cols)):
+        raise LmoeError(f"out must have shape {(M, cols)}, contiguous columns and rows that do not overlap")
+    kept = (a.elems, a.scales, a.offsets, b.elems, b.scales, out)
+    dev = _device_of(*kept)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _Elsewhere(dev, stream, *kept):
+            return mx4_gemm(a, b, swiglu, dtype, out)
+    flags = MX4_SWIGLU if swiglu else 0
+    ld = cols
+    if out is None:
+        out, flags = torch.empty((M, cols), dtype=dtype, device=a.elems.device), flags | MX4_ZERO_REST
+    elif M > 1:
+        ld = out.stride(0)
+    _check(lib().lmoe_mx4_gemm(a.elems.data_ptr(), a.scales.data_ptr(), b.elems.data_ptr(), b.scales.data_ptr(), M, N,
+                               a.cols, a.groups, None if a.offsets is None else a.offsets.data_ptr(), out.data_ptr(),
+                               dt, ld, flags, _status_word(dev), _raw_stream(dev)), "lmoe_mx4_gemm")
     return out
 
 
-_balance_scratch = None
+_balance_scratch = 0
 
 
 def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream=None):
@@ -676,32 +704,33 @@ def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream
     if scores.dim() != 2 or idx.dim() != 2:
         raise LmoeError("scores must be [T, E] and idx [T, k]")
     T, E = scores.shape
-    _dev(scores, torch.float32, (T, E), "scores")
     k = idx.shape[1]
+    dev = _device_of(scores, idx, cu_seqlens)
+    _dev(scores, torch.float32, None, "scores")
     _dev(idx, torch.int32, (T, k), "idx")
-    S = 1
-    if cu_seqlens is not None:
-        _dev(_offsets(cu_seqlens), name="cu_seqlens")
-        S = cu_seqlens.numel() - 1
-    shapes = dict(loss=((1,), torch.float32), counts=((S, E), torch.int32))
-    if grad:
-        shapes["dscores"] = ((T, E), torch.float32)
-    out = dict(out or {})
-    for n in shapes.keys() & out.keys():
-        _dev(out[n], shapes[n][1], shapes[n][0], n)
-    if _balance_scratch is None:
+    S = 1 if cu_seqlens is None else _offsets(cu_seqlens, "cu_seqlens").numel() - 1
+    given = () if out is None else tuple(out.values())
+    if stream is not None or dev != torch.cuda.current_device():
+        with _Elsewhere(dev, stream, scores, idx, cu_seqlens, *given):
+            return balance_loss(scores, idx, coef, cu_seqlens, grad, out)
+    _device_of(scores, *given)
+    if not _balance_scratch:
         n = c_size_t(0)
         _check(lib().lmoe_balance_scratch_bytes(ctypes.byref(n)), "lmoe_balance_scratch_bytes")
         _balance_scratch = n.value
-    with _OnDevice(stream, scores, idx, cu_seqlens, *(out[n] for n in shapes.keys() & out.keys())) as on:
-        for n, (shp, dt) in shapes.items():
-            if n not in out:
-                out[n] = torch.empty(shp, dtype=dt, device=scores.device)
-        scratch = torch.empty(_balance_scratch, dtype=torch.uint8, device=scores.device)
-        _check(lib().lmoe_balance_loss(_ptr(scores), _ptr(idx), T, E, k, _ptr(cu_seqlens), S, float(coef),
-                                       _ptr(out["counts"]), _ptr(out["loss"]),
-                                       _ptr(out["dscores"]) if grad else None, _ptr(scratch), _ptr(on.status),
-                                       on.ptr), "lmoe_balance_loss")
+    out = dict(out or ())
+    shapes = (("loss", (1,), torch.float32), ("counts", (S, E), torch.int32), ("dscores", (T, E), torch.float32))
+    for name, shape, dt in shapes if grad else shapes[:2]:
+        if name in out:
+            _dev(out[name], dt, shape, name)
+        else:
+            out[name] = torch.empty(shape, dtype=dt, device=scores.device)
+    scratch = torch.empty(_balance_scratch, dtype=torch.uint8, device=scores.device)
+    _check(lib().lmoe_balance_loss(scores.data_ptr(), idx.data_ptr(), T, E, k,
+                                   None if cu_seqlens is None else cu_seqlens.data_ptr(), S, float(coef),
+                                   out["counts"].data_ptr(), out["loss"].data_ptr(),
+                                   out["dscores"].data_ptr() if grad else None, scratch.data_ptr(),
+                                   _status_word(dev), _raw_stream(dev)), "lmoe_balance_loss")
     return out
 
 
