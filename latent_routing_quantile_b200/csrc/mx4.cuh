@@ -65,7 +65,8 @@ struct Mx4Tiles {
 
 constexpr int kMx4TableInts = 2 * (kMx4MaxGroups + 1) + 2 + 32;
 
-// Fills the tile table (every thread of the block takes part; ends with a barrier).  Offsets that
+// Fills the tile table (at least 256 threads, every thread of the block takes part; ends with a
+// barrier).  Offsets that
 // decrease or leave [0, rows] are recorded as LMOE_STATUS_BAD_INDEX and give no tiles at all, so no
 // access follows from them (every row then belongs to no group).
 __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* status) {
@@ -84,37 +85,51 @@ __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* sta
   int* first_row = table + kMx4MaxGroups + 1;
   int* bad = table + 2 * (kMx4MaxGroups + 1);
   int* wsum = bad + 2;
-  const int n = r.groups, tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    *bad = 0;
-    first_tile[0] = 0;
-  }
+  const int n = r.groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) *bad = 0;
   __syncthreads();
-  for (int g = tid; g <= n; g += nthr) {
-    const int v = r.offsets[g];
-    if (v < 0 || v > r.rows || (g && v < r.offsets[g - 1])) *bad = 1;
-    first_row[g] = v;
+  // the first 256 threads take four groups each (kMx4MaxGroups in all)
+  int sum = 0, tiles4[4] = {0, 0, 0, 0};
+  if (tid < 256) {
+    int v[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = r.offsets[min(tid * 4 + j, n)];
+    bool wrong = false;
+#pragma unroll
+    for (int j = 0; j < 5; ++j) wrong |= v[j] < 0 || v[j] > r.rows || (j && v[j] < v[j - 1]);
+    if (wrong) *bad = 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (tid * 4 + j <= n) first_row[tid * 4 + j] = v[j];
+      tiles4[j] = (v[j + 1] - v[j] + 127) >> 7;  // 0 past the last group
+      sum += tiles4[j];
+    }
+    if (tid == 255 && n == kMx4MaxGroups) first_row[n] = v[4];
+    int inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    sum = inc - sum;  // before this thread's groups, within the warp
   }
   __syncthreads();
   int base = 0;
-  for (int g0 = 0; g0 < n; g0 += nthr) {  // running sum of the groups' tiles, a block's width at a time
-    const int g = g0 + tid;
-    int v = g < n ? (first_row[g + 1] - first_row[g] + 127) >> 7 : 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, off);
-      if (lane >= off) v += u;
-    }
-    if (lane == 31) wsum[warp] = v;
-    __syncthreads();
-    int before = base;
-    for (int w = 0; w < (nthr >> 5); ++w) {
-      if (w < warp) before += wsum[w];
-      base += wsum[w];
-    }
-    if (g < n) first_tile[g + 1] = before + v;
-    __syncthreads();
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) sum += wsum[w];
+    base += wsum[w];
   }
+  if (tid < 256) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (tid * 4 + j <= n) first_tile[tid * 4 + j] = sum;
+      sum += tiles4[j];
+    }
+    if (tid == 255 && n == kMx4MaxGroups) first_tile[n] = sum;
+  }
+  __syncthreads();
   t.first_tile = first_tile;
   t.first_row = first_row;
   t.group_rows = t.tiles_per_group = 0;
@@ -154,31 +169,55 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float s) {
   return w;
 }
 
-// Eight values of a row as fp32; `vec`: the row starts on a 16-byte boundary.
-__device__ __forceinline__ void mx4_load8(const bf16* p, bool vec, float (&v)[8]) {
+// Eight values of a row as they are stored (bf16: four words, fp32: eight); `vec`: the row starts on a
+// 16-byte boundary.
+template <typename T>
+struct Mx4Raw {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void mx4_load8(const T* p, bool vec, Mx4Raw<T>& r) {
   if (vec) {
-    const uint4 q = ldg_nc_v4(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint4 q = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + i);
+      r.w[4 * i] = q.x;
+      r.w[4 * i + 1] = q.y;
+      r.w[4 * i + 2] = q.z;
+      r.w[4 * i + 3] = q.w;
     }
+  } else if constexpr (sizeof(T) == 2) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)h[2 * j] | ((uint32_t)h[2 * j + 1] << 16);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = bf2f(p[j]);
+    for (int j = 0; j < 8; ++j) r.w[j] = reinterpret_cast<const uint32_t*>(p)[j];
   }
 }
-__device__ __forceinline__ void mx4_load8(const float* p, bool vec, float (&v)[8]) {
-  if (vec) {
-    const uint4 a = ldg_nc_v4(p), b = ldg_nc_v4(p + 4);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// Largest magnitude of the eight values, as fp32 bits (for bf16 the low half may hold anything: only the
+// exponent is read).
+__device__ __forceinline__ uint32_t mx4_amax(const Mx4Raw<bf16>& r) {
+  const uint32_t m = __vmaxu2(__vmaxu2(r.w[0] & 0x7FFF7FFFu, r.w[1] & 0x7FFF7FFFu),
+                              __vmaxu2(r.w[2] & 0x7FFF7FFFu, r.w[3] & 0x7FFF7FFFu));
+  return max(m, m << 16);
+}
+__device__ __forceinline__ uint32_t mx4_amax(const Mx4Raw<float>& r) {
+  uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
-  } else {
+  for (int j = 0; j < 8; ++j) m = max(m, r.w[j] & 0x7FFFFFFFu);
+  return m;
+}
+__device__ __forceinline__ void mx4_floats(const Mx4Raw<bf16>& r, float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = p[j];
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(r.w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(r.w[j] & 0xFFFF0000u);
   }
+}
+__device__ __forceinline__ void mx4_floats(const Mx4Raw<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j]);
 }
 
 struct Mx4QuantParams {
@@ -193,65 +232,81 @@ struct Mx4QuantParams {
   int vec;           // every row of src starts on a 16-byte boundary
 };
 
-// A block takes one tile of 128 rows and 256 columns at a time (a grid of persistent blocks walks
-// them); a lane takes 8 of a row's 32-value blocks' values, four lanes a block, so a warp reads a
-// row's 256 values at once and writes their codes as one 128-byte line.  The tile's scale bytes
-// gather in shared memory in atom order and leave as two whole atoms.
+// Row n (0 .. 15) of slice `sl` (0 .. 7) of a tile: a slice's rows are those whose scale words lie side by
+// side in an atom (bytes 64 sl .. +63).
+__device__ __forceinline__ int mx4_slice_row(int sl, int n) { return 4 * sl + (n >> 2) + 32 * (n & 3); }
+
+// A warp takes a slice of 16 rows and 256 columns of a tile at a time; a lane holds 8 of a row's
+// values, four lanes a block of 32, so a warp reads a row's 256 values at once and writes their codes
+// as one 128-byte line.  Of the scale byte that a block's four lanes agree on, lane j keeps that of rows
+// 4 q + j; two exchanges of bytes between lanes then give each lane the four bytes of one row (half-warp
+// a: atom a, lane n of it: row n), which leave as two runs of 64 bytes.  No shared memory and no
+// barriers but for the ragged groups' table: the warps' loads overlap freely.
 // PAIRED: rows are the gate and linear projections of a SwiGLU interleaved in groups of 64 (row
 // 128 (j / 64) + j % 64 = w1[j], 64 further w3[j]).
+constexpr int kMx4Batch = 4;  // rows in flight a warp
 template <typename T, bool PAIRED>
-__global__ void __launch_bounds__(256) mx4_quant_kernel(const Mx4QuantParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) mx4_quant_kernel(const Mx4QuantParams p) {
   __shared__ int table[kMx4TableInts];
-  __shared__ __align__(16) uint8_t sf[1024];
   pdl_wait();
   pdl_trigger();
   const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int nkb = mx4_kblocks(p.cols);
-  const long long n = (long long)tiles.total * nkb;
-  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
-    const int t = (int)(u / nkb), kb = (int)(u - (long long)t * nkb);
+  const long long n = (long long)tiles.total * nkb * 8;
+  for (long long u = blockIdx.x * 8ll + (threadIdx.x >> 5); u < n; u += gridDim.x * 8ll) {
+    const int sl = (int)(u & 7);
+    const long long tk = u >> 3;
+    const int t = (int)(tk / nkb), kb = (int)(tk - (long long)t * nkb);
     int g, row0, valid;
     tiles.get(t, g, row0, valid);
-    if (threadIdx.x < 64) reinterpret_cast<uint4*>(sf)[threadIdx.x] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
     const int c = kb * 256 + lane * 8;
     const bool in = c < p.cols;  // cols is a multiple of 32: a block is inside or outside whole
-#pragma unroll 4
-    for (int r = warp; r < valid; r += 8) {
-      float v[8];
-      const int row = row0 + r;
-      if (in) {
-        if constexpr (PAIRED) {
-          // row of the interleaved matrix -> row of w1 or w3 (group g has 2h rows)
-          const int within = row - g * tiles.group_rows;
-          const long long srow = (long long)g * (tiles.group_rows >> 1) + (within >> 7) * 64 + (within & 63);
-          mx4_load8(static_cast<const T*>((within & 64) ? p.src3 : p.src) + srow * p.ld + c, p.vec, v);
-        } else {
-          mx4_load8(static_cast<const T*>(p.src) + (long long)row * p.ld + c, p.vec, v);
+    uint32_t word = 0;
+#pragma unroll
+    for (int b = 0; b < 16; b += kMx4Batch) {
+      Mx4Raw<T> raw[kMx4Batch];
+#pragma unroll
+      for (int i = 0; i < kMx4Batch; ++i) {
+        const int r = mx4_slice_row(sl, b + i);
+#pragma unroll
+        for (int j = 0; j < (int)(2 * sizeof(T)); ++j) raw[i].w[j] = 0;
+        if (in && r < valid) {
+          const int row = row0 + r;
+          if constexpr (PAIRED) {
+            // row of the interleaved matrix -> row of w1 or w3 (group g has 2h rows)
+            const int within = row - g * tiles.group_rows;
+            const long long srow = (long long)g * (tiles.group_rows >> 1) + (within >> 7) * 64 + (within & 63);
+            mx4_load8(static_cast<const T*>((within & 64) ? p.src3 : p.src) + srow * p.ld + c, p.vec, raw[i]);
+          } else {
+            mx4_load8(static_cast<const T*>(p.src) + (long long)row * p.ld + c, p.vec, raw[i]);
+          }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
       }
-      uint32_t amax = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const uint32_t sb = mx4_scale_byte(amax);
-      // 2^-X = 2^(127 - byte): exponent field 254 - byte, at least 2 for every finite block
-      const float s = __uint_as_float((254u - min(sb, 252u)) << 23);
-      if (in) {
-        *reinterpret_cast<uint32_t*>(p.elems + (long long)row * (p.cols >> 1) + (c >> 1)) = e2m1x8(v, s);
-        if ((lane & 3) == 0)
-          sf[(lane >> 4) * 512 + 16 * (r & 31) + 4 * (r >> 5) + ((lane >> 2) & 3)] = (uint8_t)sb;
+      for (int i = 0; i < kMx4Batch; ++i) {
+        const int r = mx4_slice_row(sl, b + i);
+        uint32_t amax = mx4_amax(raw[i]);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t sb = mx4_scale_byte(amax);
+        // 2^-X = 2^(127 - byte): exponent field 254 - byte, at least 2 for every finite block
+        const float s = __uint_as_float((254u - min(sb, 252u)) << 23);
+        if (in && r < valid) {
+          float v[8];
+          mx4_floats(raw[i], v);
+          *reinterpret_cast<uint32_t*>(p.elems + (long long)(row0 + r) * (p.cols >> 1) + (c >> 1)) = e2m1x8(v, s);
+        }
+        if ((lane & 3) == ((b + i) & 3)) word |= sb << (8 * ((b + i) >> 2));
       }
     }
-    __syncthreads();
-    if (threadIdx.x < 64)
-      reinterpret_cast<uint4*>(p.scales + u * 1024)[threadIdx.x] = reinterpret_cast<uint4*>(sf)[threadIdx.x];
-    __syncthreads();
+    // bytes (block (lane >> 2) & 3, q = 0 .. 3) -> (row 4 ((lane >> 2) & 3) + lane % 4, block = 0 .. 3)
+    uint32_t y = __shfl_xor_sync(0xffffffffu, word, 4);
+    word = __byte_perm(word, y, (lane & 4) ? 0x3715 : 0x6240);
+    y = __shfl_xor_sync(0xffffffffu, word, 8);
+    word = __byte_perm(word, y, (lane & 8) ? 0x3276 : 0x5410);
+    // row n of the slice: byte 16 (4 sl + n / 4) + 4 (n % 4) = 64 sl + 4 n of its atom
+    *reinterpret_cast<uint32_t*>(p.scales + tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15)) = word;
   }
 }
 
@@ -276,7 +331,7 @@ __device__ __forceinline__ float e2m1_value(uint32_t c, float s) {
   return ((c & 8u) ? -a : a) * s;
 }
 
-// Same tiles and lanes as the quantisation.
+// Same slices and lanes as the quantisation.
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_dequant_kernel(const Mx4DequantParams p) {
   __shared__ int table[kMx4TableInts];
@@ -285,26 +340,37 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(const Mx4DequantParams
   const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkb = mx4_kblocks(p.cols);
-  const long long n = (long long)tiles.total * nkb;
-  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
-    const int t = (int)(u / nkb), kb = (int)(u - (long long)t * nkb);
+  const long long n = (long long)tiles.total * nkb * 8;
+  for (long long u = blockIdx.x * 8ll + warp; u < n; u += gridDim.x * 8ll) {
+    const int sl = (int)(u & 7);
+    const long long tk = u >> 3;
+    const int t = (int)(tk / nkb), kb = (int)(tk - (long long)t * nkb);
     int g, row0, valid;
     tiles.get(t, g, row0, valid);
     const int c = kb * 256 + lane * 8;
-    if (c >= p.cols) continue;
-    const uint8_t* sf = p.scales + u * 1024 + (lane >> 4) * 512 + ((lane >> 2) & 3);
-#pragma unroll 4
-    for (int r = warp; r < valid; r += 8) {
-      const long long row = row0 + r;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p.elems + row * (p.cols >> 1) + (c >> 1));
-      const uint32_t sb = sf[16 * (r & 31) + 4 * (r >> 5)];
+    const bool in = c < p.cols;
+    const uint32_t word =
+        *reinterpret_cast<const uint32_t*>(p.scales + tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15));
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = mx4_slice_row(sl, i);
+      w[i] = 0;
+      if (in && r < valid)
+        w[i] = *reinterpret_cast<const uint32_t*>(p.elems + (long long)(row0 + r) * (p.cols >> 1) + (c >> 1));
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = mx4_slice_row(sl, i);
+      const uint32_t sb = (__shfl_sync(0xffffffffu, word, (lane & 16) + i) >> (8 * ((lane >> 2) & 3))) & 255u;
       // 2^(byte - 127): a subnormal for byte 0, NaN for 255
       const float s = sb == 255u ? __uint_as_float(0x7FC00000u)
                                  : (sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u));
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e2m1_value(w >> (4 * j), s);
-      T* o = static_cast<T*>(p.out) + row * p.ld + c;
+      for (int j = 0; j < 8; ++j) v[j] = e2m1_value(w[i] >> (4 * j), s);
+      if (!in || r >= valid) continue;
+      T* o = static_cast<T*>(p.out) + (long long)(row0 + r) * p.ld + c;
       if (p.vec) {
         if constexpr (sizeof(T) == 4) {
           reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);

@@ -27,8 +27,14 @@ int check_rows(int64_t rows, int32_t cols, int32_t groups, bool ragged) {
   if (cols % 32 || groups > kMx4MaxGroups || rows > (1ll << 30)) return LMOE_EUNSUPPORTED;
   return LMOE_OK;
 }
+// Row tiles the scale buffer has room for: ragged groups hold at most rows / 128 whole tiles and one
+// partial tile each.
 long long scale_tiles(int64_t rows, int32_t groups, bool ragged) {
   return ragged ? (rows + 127) / 128 + groups : (rows / groups + 127) / 128 * groups;
+}
+// Row tiles a call can have: a group without rows has none.
+long long work_tiles(int64_t rows, int32_t groups, bool ragged) {
+  return ragged ? rows / 128 + std::min<int64_t>(groups, rows) : scale_tiles(rows, groups, false);
 }
 
 template <typename T>
@@ -36,11 +42,9 @@ bool rows16(const void* p, int64_t ld) {
   return ((uintptr_t)p & 15) == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
 }
 
-// Persistent grid of the quantisation kernels: four blocks of 256 threads an SM.
-int mx4_grid(long long tiles, int nkb, int sms) {
-  const long long n = tiles * nkb;
-  return (int)(n < 4ll * sms ? (n < 1 ? 1 : n) : 4ll * sms);
-}
+// Persistent grid of the quantisation kernels (eight warps a block, a block a tile and k-block): at
+// most eight blocks an SM.
+int mx4_grid(long long tiles, int nkb, int sms) { return (int)std::min(tiles * nkb, 8ll * sms); }
 
 }  // namespace
 
@@ -78,7 +82,7 @@ int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32
   p.scales = scales;
   p.status = status;
   p.vec = dtype == LMOE_F32 ? rows16<float>(x, ld) : rows16<bf16>(x, ld);
-  const int grid = mx4_grid(scale_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
+  const int grid = mx4_grid(work_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
     CK(launch_k(mx4_quant_kernel<float, false>, dim3(grid), dim3(256), 0, st, 1, p));
@@ -112,7 +116,7 @@ int lmoe_mx4_quant_w13(const void* w1, const void* w3, int32_t dtype, int32_t gr
   p.scales = scales;
   p.status = status;
   p.vec = (((uintptr_t)w1 | (uintptr_t)w3) & 15) == 0;  // cols is a multiple of 32
-  const int grid = mx4_grid(scale_tiles(rows, groups, false), mx4_kblocks(cols), sms);
+  const int grid = mx4_grid(work_tiles(rows, groups, false), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
     CK(launch_k(mx4_quant_kernel<float, true>, dim3(grid), dim3(256), 0, st, 1, p));
@@ -145,7 +149,7 @@ int lmoe_mx4_dequant(const uint8_t* elems, const uint8_t* scales, int64_t rows, 
   p.status = status;
   p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
   p.vec = dtype == LMOE_F32 ? rows16<float>(out, ld) : rows16<bf16>(out, ld);
-  const int grid = mx4_grid(scale_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
+  const int grid = mx4_grid(work_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
     CK(launch_k(mx4_dequant_kernel<float>, dim3(grid), dim3(256), 0, st, 1, p));
@@ -190,7 +194,7 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
   p.vec = c_dtype == LMOE_F32 ? rows16<float>(c, ldc) : rows16<bf16>(c, ldc);
   p.status = status;
-  const long long tiles = scale_tiles(M, groups, offsets != nullptr) * p.n_tiles;
+  const long long tiles = work_tiles(M, groups, offsets != nullptr) * p.n_tiles;
   const int grid = (int)(tiles < sms ? tiles : sms);
   cudaStream_t st = (cudaStream_t)stream;
   auto run = [&](auto kern, unsigned& done) -> int {
