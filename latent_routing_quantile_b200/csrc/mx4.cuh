@@ -37,21 +37,26 @@ struct Mx4Rows {
 // Tiles of 128 rows, group by group.  Ragged groups need a prefix sum over the groups, which each
 // block makes once in shared memory.
 struct Mx4Tiles {
-  const int* first_tile;  // shared, [groups + 1] (ragged groups)
-  const int* first_row;   // shared, [groups + 1]
+  const int* first_row;      // shared, [groups + 1] (ragged groups)
+  const uint16_t* partial;   // shared, [groups + 1]: partial tiles, see first_tile
   int groups, group_rows, tiles_per_group, total;
   int rest_lo, rest_hi;   // rows [0, rest_lo) and [rest_hi, rows) belong to no group
 
-  // Group, first row and valid rows of tile t.
+  // First tile of group g: the whole tiles that its distance from the first row would make, and what
+  // rounding each group up to whole tiles adds to them, which is at most one a group (16 bits).
+  __device__ __forceinline__ int first_tile(int g) const { return ((first_row[g] - first_row[0]) >> 7) + partial[g]; }
+  // Group, first row and valid rows of tile t; the whole warp takes part (two rounds of 32 groups
+  // compared at once).
   __device__ __forceinline__ void get(int t, int& g, int& row0, int& valid) const {
-    if (first_tile) {
-      int lo = 0, hi = groups;  // first_tile[lo] <= t < first_tile[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_tile[mid] <= t) lo = mid; else hi = mid;
-      }
-      g = lo;
-      const int within = (t - first_tile[g]) * 128;
+    if (first_row) {
+      // the last group whose first tile is at most t (groups without rows begin where the next one does)
+      const int lane = threadIdx.x & 31;
+      const int step = (groups + 31) >> 5;
+      const int a = lane * step;
+      const int base = (__popc(__ballot_sync(0xffffffffu, a < groups && first_tile(a) <= t)) - 1) * step;
+      const int b = base + lane;
+      g = base + __popc(__ballot_sync(0xffffffffu, lane < step && b < groups && first_tile(b) <= t)) - 1;
+      const int within = (t - first_tile(g)) * 128;
       row0 = first_row[g] + within;
       valid = min(128, first_row[g + 1] - row0);
     } else {
@@ -63,7 +68,7 @@ struct Mx4Tiles {
   }
 };
 
-constexpr int kMx4TableInts = 2 * (kMx4MaxGroups + 1) + 2 + 32;
+constexpr int kMx4TableInts = (kMx4MaxGroups + 1) + (kMx4MaxGroups + 2) / 2 + 1 + 8;
 
 // Fills the tile table (at least 256 threads, every thread of the block takes part; ends with a
 // barrier).  Offsets that
@@ -73,7 +78,8 @@ __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* sta
   Mx4Tiles t;
   t.groups = r.groups;
   if (!r.offsets) {
-    t.first_tile = t.first_row = nullptr;
+    t.first_row = nullptr;
+    t.partial = nullptr;
     t.group_rows = r.rows / r.groups;
     t.tiles_per_group = (t.group_rows + 127) >> 7;
     t.total = t.tiles_per_group * r.groups;
@@ -81,15 +87,15 @@ __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* sta
     t.rest_hi = r.rows;
     return t;
   }
-  int* first_tile = table;
-  int* first_row = table + kMx4MaxGroups + 1;
-  int* bad = table + 2 * (kMx4MaxGroups + 1);
-  int* wsum = bad + 2;
+  int* first_row = table;
+  uint16_t* partial = reinterpret_cast<uint16_t*>(table + kMx4MaxGroups + 1);
+  int* bad = table + (kMx4MaxGroups + 1) + (kMx4MaxGroups + 2) / 2;
+  int* wsum = bad + 1;
   const int n = r.groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) *bad = 0;
   __syncthreads();
   // the first 256 threads take four groups each (kMx4MaxGroups in all)
-  int sum = 0, tiles4[4] = {0, 0, 0, 0};
+  int sum = 0, own[4] = {0, 0, 0, 0};
   if (tid < 256) {
     int v[5];
 #pragma unroll
@@ -99,12 +105,13 @@ __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* sta
     for (int j = 0; j < 5; ++j) wrong |= v[j] < 0 || v[j] > r.rows || (j && v[j] < v[j - 1]);
     if (wrong) *bad = 1;
 #pragma unroll
+    for (int j = 0; j < 5; ++j)
+      if (tid * 4 + j <= n && (j < 4 || tid == 255)) first_row[tid * 4 + j] = v[j];
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (tid * 4 + j <= n) first_row[tid * 4 + j] = v[j];
-      tiles4[j] = (v[j + 1] - v[j] + 127) >> 7;  // 0 past the last group
-      sum += tiles4[j];
+      own[j] = wrong ? 0 : (v[j + 1] - v[j] + 127) >> 7;  // 0 past the last group
+      sum += own[j];
     }
-    if (tid == 255 && n == kMx4MaxGroups) first_row[n] = v[4];
     int inc = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -123,15 +130,15 @@ __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* sta
   }
   if (tid < 256) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (tid * 4 + j <= n) first_tile[tid * 4 + j] = sum;
-      sum += tiles4[j];
+    for (int j = 0; j < 5; ++j) {
+      const int g = tid * 4 + j;
+      if (g <= n && (j < 4 || tid == 255)) partial[g] = (uint16_t)(sum - ((first_row[g] - first_row[0]) >> 7));
+      if (j < 4) sum += own[j];
     }
-    if (tid == 255 && n == kMx4MaxGroups) first_tile[n] = sum;
   }
   __syncthreads();
-  t.first_tile = first_tile;
   t.first_row = first_row;
+  t.partial = partial;
   t.group_rows = t.tiles_per_group = 0;
   t.total = *bad ? 0 : base;
   t.rest_lo = *bad ? r.rows : first_row[0];
@@ -252,12 +259,12 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) mx4_quant_kernel(
   pdl_trigger();
   const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
   const int lane = threadIdx.x & 31;
-  const int nkb = mx4_kblocks(p.cols);
-  const long long n = (long long)tiles.total * nkb * 8;
-  for (long long u = blockIdx.x * 8ll + (threadIdx.x >> 5); u < n; u += gridDim.x * 8ll) {
+  const unsigned nkb = (unsigned)mx4_kblocks(p.cols);
+  const unsigned n = (unsigned)tiles.total * nkb * 8;  // less than 2^31, as the host has seen to
+  for (unsigned u = blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += gridDim.x * 8) {
     const int sl = (int)(u & 7);
-    const long long tk = u >> 3;
-    const int t = (int)(tk / nkb), kb = (int)(tk - (long long)t * nkb);
+    const unsigned tk = u >> 3;
+    const int t = (int)(tk / nkb), kb = (int)(tk - t * nkb);
     int g, row0, valid;
     tiles.get(t, g, row0, valid);
     const int c = kb * 256 + lane * 8;
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) mx4_quant_kernel(
     y = __shfl_xor_sync(0xffffffffu, word, 8);
     word = __byte_perm(word, y, (lane & 8) ? 0x3276 : 0x5410);
     // row n of the slice: byte 16 (4 sl + n / 4) + 4 (n % 4) = 64 sl + 4 n of its atom
-    *reinterpret_cast<uint32_t*>(p.scales + tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15)) = word;
+    *reinterpret_cast<uint32_t*>(p.scales + (size_t)tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15)) = word;
   }
 }
 
@@ -323,65 +330,70 @@ struct Mx4DequantParams {
   int zero_rest;     // 1: rows of no group are set to zero
 };
 
-// The value of code c (4 bits) times 2^X.  E2M1 is widened to fp32 by its bits: exponent field e, one
-// mantissa bit m: e > 0: (1 + m/2) 2^(e-1); e = 0: m/2.
-__device__ __forceinline__ float e2m1_value(uint32_t c, float s) {
-  const uint32_t m = c & 7u;
-  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float((((m >> 1) + 126u) << 23) | ((m & 1u) << 22));
-  return ((c & 8u) ? -a : a) * s;
+// The values of eight codes (the first in the lowest four bits) times s; fp16 holds every code's value.
+__device__ __forceinline__ void e2m1_values(uint32_t w, float s, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * j)), __NV_E2M1);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * j] = f.x * s;
+    v[2 * j + 1] = f.y * s;
+  }
 }
 
 // Same slices and lanes as the quantisation.
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_dequant_kernel(const Mx4DequantParams p) {
+__global__ void __launch_bounds__(256, 5) mx4_dequant_kernel(const Mx4DequantParams p) {
   __shared__ int table[kMx4TableInts];
   pdl_wait();
   pdl_trigger();
   const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nkb = mx4_kblocks(p.cols);
-  const long long n = (long long)tiles.total * nkb * 8;
-  for (long long u = blockIdx.x * 8ll + warp; u < n; u += gridDim.x * 8ll) {
+  const unsigned nkb = (unsigned)mx4_kblocks(p.cols);
+  const unsigned n = (unsigned)tiles.total * nkb * 8;
+  for (unsigned u = blockIdx.x * 8 + warp; u < n; u += gridDim.x * 8) {
     const int sl = (int)(u & 7);
-    const long long tk = u >> 3;
-    const int t = (int)(tk / nkb), kb = (int)(tk - (long long)t * nkb);
+    const unsigned tk = u >> 3;
+    const int t = (int)(tk / nkb), kb = (int)(tk - t * nkb);
     int g, row0, valid;
     tiles.get(t, g, row0, valid);
     const int c = kb * 256 + lane * 8;
     const bool in = c < p.cols;
     const uint32_t word =
-        *reinterpret_cast<const uint32_t*>(p.scales + tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15));
-    uint32_t w[16];
+        *reinterpret_cast<const uint32_t*>(p.scales + (size_t)tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15));
+#pragma unroll 1
+    for (int b = 0; b < 16; b += 8) {
+      uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = mx4_slice_row(sl, i);
-      w[i] = 0;
-      if (in && r < valid)
-        w[i] = *reinterpret_cast<const uint32_t*>(p.elems + (long long)(row0 + r) * (p.cols >> 1) + (c >> 1));
-    }
+      for (int i = 0; i < 8; ++i) {
+        const int r = mx4_slice_row(sl, b + i);
+        w[i] = 0;
+        if (in && r < valid)
+          w[i] = *reinterpret_cast<const uint32_t*>(p.elems + (long long)(row0 + r) * (p.cols >> 1) + (c >> 1));
+      }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = mx4_slice_row(sl, i);
-      const uint32_t sb = (__shfl_sync(0xffffffffu, word, (lane & 16) + i) >> (8 * ((lane >> 2) & 3))) & 255u;
-      // 2^(byte - 127): a subnormal for byte 0, NaN for 255
-      const float s = sb == 255u ? __uint_as_float(0x7FC00000u)
-                                 : (sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u));
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e2m1_value(w[i] >> (4 * j), s);
-      if (!in || r >= valid) continue;
-      T* o = static_cast<T*>(p.out) + (long long)(row0 + r) * p.ld + c;
-      if (p.vec) {
-        if constexpr (sizeof(T) == 4) {
-          reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-          reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      for (int i = 0; i < 8; ++i) {
+        const int r = mx4_slice_row(sl, b + i);
+        const uint32_t sb = (__shfl_sync(0xffffffffu, word, (lane & 16) + b + i) >> (8 * ((lane >> 2) & 3))) & 255u;
+        // 2^(byte - 127): a subnormal for byte 0, NaN for 255
+        const float s = sb == 255u ? __uint_as_float(0x7FC00000u)
+                                   : (sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u));
+        float v[8];
+        e2m1_values(w[i], s, v);
+        if (!in || r >= valid) continue;
+        T* o = static_cast<T*>(p.out) + (long long)(row0 + r) * p.ld + c;
+        if (p.vec) {
+          if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+            *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          }
         } else {
-          *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-        }
-      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = from_f<T>(v[j]);
+          for (int j = 0; j < 8; ++j) o[j] = from_f<T>(v[j]);
+        }
       }
     }
   }

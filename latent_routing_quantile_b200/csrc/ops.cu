@@ -1,7 +1,9 @@
 // Host side of the entry points that need no layer handle and work on the caller's buffers: MXFP4
 // quantisation, dequantisation and products, and the router's balance loss.
 #include <algorithm>
+#include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include "balance.cuh"
 #include "host.cuh"
@@ -20,17 +22,18 @@ int device_sms(int* sms) {
   return major == 10 ? LMOE_OK : LMOE_EDEVICE;
 }
 
-// Sizes of a matrix in groups: rows and 128-row tiles stay within 32-bit indices.
-int check_rows(int64_t rows, int32_t cols, int32_t groups, bool ragged) {
-  if (rows < 0 || cols <= 0 || groups <= 0) return LMOE_EINVAL;
-  if (!ragged && rows % groups) return LMOE_EINVAL;
-  if (cols % 32 || groups > kMx4MaxGroups || rows > (1ll << 30)) return LMOE_EUNSUPPORTED;
-  return LMOE_OK;
-}
 // Row tiles the scale buffer has room for: ragged groups hold at most rows / 128 whole tiles and one
 // partial tile each.
 long long scale_tiles(int64_t rows, int32_t groups, bool ragged) {
   return ragged ? (rows + 127) / 128 + groups : (rows / groups + 127) / 128 * groups;
+}
+// Sizes of a matrix in groups.  The kernels count rows, and tiles x k-blocks x 8 slices, in 32 bits.
+int check_rows(int64_t rows, int32_t cols, int32_t groups, bool ragged) {
+  if (rows < 0 || cols <= 0 || groups <= 0) return LMOE_EINVAL;
+  if (!ragged && rows % groups) return LMOE_EINVAL;
+  if (cols % 32 || groups > kMx4MaxGroups || rows > (1ll << 30)) return LMOE_EUNSUPPORTED;
+  if (scale_tiles(rows, groups, ragged) * mx4_kblocks(cols) * 8 >= (1ll << 31)) return LMOE_EUNSUPPORTED;
+  return LMOE_OK;
 }
 // Row tiles a call can have: a group without rows has none.
 long long work_tiles(int64_t rows, int32_t groups, bool ragged) {
@@ -45,6 +48,63 @@ bool rows16(const void* p, int64_t ld) {
 // Persistent grid of the quantisation kernels (eight warps a block, a block a tile and k-block): at
 // most eight blocks an SM.
 int mx4_grid(long long tiles, int nkb, int sms) { return (int)std::min(tiles * nkb, 8ll * sms); }
+
+// Tensor map of a matrix's scale atoms: `tiles` row tiles of nkb k-blocks of 1 KB (two atoms), as rows of
+// 128 bytes; a box is one k-block of `box_tiles` row tiles.
+bool make_map_atoms(CUtensorMap* m, const uint8_t* scales, long long tiles, int nkb, int box_tiles) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || tiles <= 0) return false;
+  cuuint64_t dims[3] = {128, (cuuint64_t)nkb * 8, (cuuint64_t)tiles};
+  cuuint64_t strides[2] = {128, (cuuint64_t)nkb * 1024};
+  cuuint32_t box[3] = {128, 8, (cuuint32_t)box_tiles};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(scales), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map of a product's result: boxes of one staging round, rows of `words` words (64 bytes: 64-byte
+// swizzle, 128: 128-byte).
+bool make_map_c(CUtensorMap* m, void* c, long long rows, int cols, long long ld, bool f32, int words) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int es_bytes = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld * es_bytes)};
+  cuuint32_t box[2] = {(cuuint32_t)(4 * words / es_bytes), (cuuint32_t)mx4_round_rows(words)};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, words == 16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool GLU, int BN>
+int launch_mx4_gemm(const Mx4GemmParams& p, int grid, cudaStream_t st) {
+  auto kern = mx4_gemm_kernel<T, GLU, BN>;
+  static unsigned done = 0;
+  constexpr int smem = Mx4Cfg<BN>::kSmemBytes;
+  CK(ensure_smem_attr(kern, smem, done));
+  CK(launch_k(kern, dim3(grid), dim3(kMx4Threads), smem, st, p.split, p));
+  return LMOE_OK;
+}
+
+// How a product is cut (see mx4_gemm.cuh).
+struct Mx4Plan {
+  int bn, split, grid;
+};
+Mx4Plan plan_mx4(int M, int N, int nkb, int groups, bool ragged, int sms) {
+  const long long mt = work_tiles(M, groups, ragged);
+  const long long t128 = mt * ((N + 127) / 128), t256 = mt * ((N + 255) / 256);
+  const int fs = getenv("MX4_SPLIT") ? atoi(getenv("MX4_SPLIT")) : 0;
+  if (fs) return {128, fs, (int)t128 * fs};
+  // 256-wide tiles where they take fewer waves of the GPU by more than their longer k-blocks cost
+  if ((t256 + sms - 1) / sms * 3 <= (t128 + sms - 1) / sms * 2)
+    return {256, 1, (int)std::min<long long>(t256, sms)};
+  int split = 1;
+  if (nkb >= 12)
+    while (split < 8 && nkb >= 8 * split && 2 * split * t128 <= sms) split *= 2;
+  return {128, split, (int)std::min<long long>(t128 * split, sms)};
+}
 
 }  // namespace
 
@@ -168,6 +228,7 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   int rc = check_rows(M, K, groups, offsets != nullptr);
   if (!rc) rc = check_rows((int64_t)groups * N, K, groups, false);
   if (rc) return rc;
+  if (scale_tiles(M, groups, offsets != nullptr) * ((N + 127) / 128) >= (1ll << 31)) return LMOE_EUNSUPPORTED;
   if (swiglu && (N % 128 || c_dtype != LMOE_BF16)) return LMOE_EUNSUPPORTED;
   if (M == 0) return LMOE_OK;
   const int32_t cols = swiglu ? N / 2 : N;
@@ -177,35 +238,38 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   int sms = 0;
   rc = device_sms(&sms);
   if (rc) return rc;
+  const int nkb = mx4_kblocks(K);
+  const Mx4Plan plan = plan_mx4(M, N, nkb, groups, offsets != nullptr, sms);
   Mx4GemmParams p;
   memset(&p, 0, sizeof(p));
-  if (!make_map_u8(&p.tmA, a_elems, M, K / 2, K / 2, 128) ||
-      !make_map_u8(&p.tmB, b_elems, (long long)groups * N, K / 2, K / 2, 128))
+  p.b_tiles = (N + 127) / 128;
+  if (!make_map_u8(&p.tmA, a_elems, M, K / 2, K / 2, 128) || !make_map_u8(&p.tmA32, a_elems, M, K / 2, K / 2, 32) ||
+      !make_map_u8(&p.tmB, b_elems, (long long)groups * N, K / 2, K / 2, 128) ||
+      !make_map_atoms(&p.tmSA, a_scales, scale_tiles(M, groups, offsets != nullptr), nkb, 1) ||
+      !make_map_atoms(&p.tmSB, b_scales, (long long)groups * p.b_tiles, nkb, plan.bn / 128))
     return LMOE_ECUDA;
-  p.a_sf = a_scales;
-  p.b_sf = b_scales;
   p.rows = Mx4Rows{offsets, groups, M};
   p.N = N;
-  p.n_tiles = (N + 127) / 128;
-  p.nkb = mx4_kblocks(K);
+  p.n_tiles = (N + plan.bn - 1) / plan.bn;
+  p.nkb = nkb;
+  p.split = plan.split;
   p.c = c;
   p.ldc = ldc;
   p.c_cols = cols;
   p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
   p.vec = c_dtype == LMOE_F32 ? rows16<float>(c, ldc) : rows16<bf16>(c, ldc);
   p.status = status;
-  const long long tiles = work_tiles(M, groups, offsets != nullptr) * p.n_tiles;
-  const int grid = (int)(tiles < sms ? tiles : sms);
+  if (p.vec && !make_map_c(&p.tmC, c, M, cols, ldc, c_dtype == LMOE_F32, swiglu ? 16 : 32)) return LMOE_ECUDA;
   cudaStream_t st = (cudaStream_t)stream;
-  auto run = [&](auto kern, unsigned& done) -> int {
-    CK(ensure_smem_attr(kern, kMx4SmemBytes, done));
-    CK(launch_k(kern, dim3(grid), dim3(kMx4Threads), kMx4SmemBytes, st, 1, p));
-    return LMOE_OK;
+  auto launch = [&](auto type, auto glu) -> int {
+    using T = decltype(type);
+    constexpr bool G = decltype(glu)::value;
+    if (plan.bn == 256) return launch_mx4_gemm<T, G, 256>(p, plan.grid, st);
+    return launch_mx4_gemm<T, G, 128>(p, plan.grid, st);
   };
-  static unsigned done[3] = {0, 0, 0};
-  if (swiglu) return run(mx4_gemm_kernel<bf16, true>, done[0]);
-  if (c_dtype == LMOE_BF16) return run(mx4_gemm_kernel<bf16, false>, done[1]);
-  return run(mx4_gemm_kernel<float, false>, done[2]);
+  if (swiglu) return launch(bf16(), std::true_type());
+  if (c_dtype == LMOE_BF16) return launch(bf16(), std::false_type());
+  return launch(0.f, std::false_type());
 }
 
 int lmoe_balance_scratch_bytes(size_t* bytes) {
