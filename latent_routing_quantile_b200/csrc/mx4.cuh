@@ -17,7 +17,9 @@
 // the scales of two groups, wherever the groups begin in the elements.
 #pragma once
 
-#include <cuda_fp4.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -159,72 +161,96 @@ __device__ __forceinline__ void mx4_zero_rest(const Mx4Tiles& t, int rows, T* ou
 }
 
 // --------------------------------------------------------------------------- quantisation
-// Scale byte of a block whose largest magnitude has the fp32 bits `amax` (NaN and infinity compare
-// above every number): the exponent field less 2, so that the largest value lands in [4, 8).
-__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax) {
-  const int e = (int)(amax >> 23);
-  return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
-}
-
-// Eight values, scaled, as eight codes (the first in the lowest four bits).
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float s) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * j] * s, v[2 * j + 1] * s), __NV_E2M1, cudaRoundNearest)
-         << (8 * j);
+// Eight values as eight codes (the first in the lowest four bits), to nearest, ties to even, saturating.
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return w;
 }
 
-// Eight values of a row as they are stored (bf16: four words, fp32: eight); `vec`: the row starts on a
-// 16-byte boundary.
+// How rows are read and written: 32 bytes at a time, 16, or element by element, by what every row's
+// address is a multiple of.
+enum Mx4Access : int { MX4_ELEMENTS = 0, MX4_16 = 1, MX4_32 = 2 };
+
+// Sixteen values of a row as they are stored (bf16: eight words, fp32: sixteen).
 template <typename T>
 struct Mx4Raw {
-  uint32_t w[2 * sizeof(T)];
+  uint32_t w[4 * sizeof(T)];
 };
 template <typename T>
-__device__ __forceinline__ void mx4_load8(const T* p, bool vec, Mx4Raw<T>& r) {
-  if (vec) {
+__device__ __forceinline__ void mx4_load16(const T* p, int access, Mx4Raw<T>& r) {
+  constexpr int kWords = 4 * sizeof(T);
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+  if (access == MX4_32) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      const uint4 q = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + i);
-      r.w[4 * i] = q.x;
-      r.w[4 * i + 1] = q.y;
-      r.w[4 * i + 2] = q.z;
-      r.w[4 * i + 3] = q.w;
+    for (int i = 0; i < kWords; i += 8)
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r.w[i]), "=r"(r.w[i + 1]), "=r"(r.w[i + 2]), "=r"(r.w[i + 3]), "=r"(r.w[i + 4]),
+                     "=r"(r.w[i + 5]), "=r"(r.w[i + 6]), "=r"(r.w[i + 7])
+                   : "l"(q + i));
+  } else if (access == MX4_16) {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) {
+      const uint4 v = ldg_nc_v4(q + i);
+      r.w[i] = v.x;
+      r.w[i + 1] = v.y;
+      r.w[i + 2] = v.z;
+      r.w[i + 3] = v.w;
     }
   } else if constexpr (sizeof(T) == 2) {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)h[2 * j] | ((uint32_t)h[2 * j + 1] << 16);
+    for (int j = 0; j < kWords; ++j) r.w[j] = (uint32_t)h[2 * j] | ((uint32_t)h[2 * j + 1] << 16);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r.w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+    for (int j = 0; j < kWords; ++j) r.w[j] = q[j];
   }
 }
-// Largest magnitude of the eight values, as fp32 bits (for bf16 the low half may hold anything: only the
-// exponent is read).
-__device__ __forceinline__ uint32_t mx4_amax(const Mx4Raw<bf16>& r) {
-  const uint32_t m = __vmaxu2(__vmaxu2(r.w[0] & 0x7FFF7FFFu, r.w[1] & 0x7FFF7FFFu),
-                              __vmaxu2(r.w[2] & 0x7FFF7FFFu, r.w[3] & 0x7FFF7FFFu));
-  return max(m, m << 16);
-}
-__device__ __forceinline__ uint32_t mx4_amax(const Mx4Raw<float>& r) {
+// Exponent field of the largest magnitude of a block: two lanes' sixteen values each (255: it holds a NaN
+// or an infinity, which compare above every number as integers).
+__device__ __forceinline__ uint32_t mx4_exponent(const Mx4Raw<bf16>& r) {
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, r.w[j] & 0x7FFFFFFFu);
-  return m;
+  for (int j = 0; j < 8; ++j) m = __vmaxu2(m, r.w[j] & 0x7FFF7FFFu);
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m >> 23, (m >> 7) & 0xFFu);
 }
-__device__ __forceinline__ void mx4_floats(const Mx4Raw<bf16>& r, float (&v)[8]) {
+__device__ __forceinline__ uint32_t mx4_exponent(const Mx4Raw<float>& r) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(r.w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(r.w[j] & 0xFFFF0000u);
+  for (int j = 0; j < 16; ++j) m = max(m, r.w[j] & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return m >> 23;
+}
+// Codes of the sixteen values times 2^-X, whose exponent field is 256 - e (e: the block's, at least 2).
+// bf16 values are scaled two at a time: exact, but for results far below the smallest code, which stay
+// there.
+__device__ __forceinline__ uint2 mx4_codes(const Mx4Raw<bf16>& r, uint32_t e) {
+  const uint32_t s = ((256u - e) << 7) * 0x10001u;
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r.w[j]),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&s));
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&x);
+    v[2 * j] = __uint_as_float(w << 16);
+    v[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
   }
+  return make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
-__device__ __forceinline__ void mx4_floats(const Mx4Raw<float>& r, float (&v)[8]) {
+__device__ __forceinline__ uint2 mx4_codes(const Mx4Raw<float>& r, uint32_t e) {
+  const float s = __uint_as_float((256u - e) << 23);
+  float v[16];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j]);
+  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r.w[j]) * s;
+  return make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
 
 struct Mx4QuantParams {
@@ -236,84 +262,93 @@ struct Mx4QuantParams {
   uint8_t* elems;
   uint8_t* scales;
   uint32_t* status;
-  int vec;           // every row of src starts on a 16-byte boundary
+  int access;        // Mx4Access of src
 };
 
-// Row n (0 .. 15) of slice `sl` (0 .. 7) of a tile: a slice's rows are those whose scale words lie side by
-// side in an atom (bytes 64 sl .. +63).
-__device__ __forceinline__ int mx4_slice_row(int sl, int n) { return 4 * sl + (n >> 2) + 32 * (n & 3); }
+// A tile's rows fall into eight slices of 16: row n of slice sl is row 4 sl + n / 4 + 32 (n % 4), so that
+// a slice's scale words lie side by side in an atom (bytes 64 sl .. +63).  A warp takes a slice and 256
+// columns of a tile at a time, half a warp a row: a lane reads 16 of its values and writes their eight
+// bytes of codes, two lanes make a block of 32.  Lanes of a half: bit 3 the atom a, bits 1-2 the block b
+// in it, bit 0 the lane j of the block.
+__device__ __forceinline__ constexpr int mx4_row(int n) { return (n >> 2) + 32 * (n & 3); }
 
-// A warp takes a slice of 16 rows and 256 columns of a tile at a time; a lane holds 8 of a row's
-// values, four lanes a block of 32, so a warp reads a row's 256 values at once and writes their codes
-// as one 128-byte line.  Of the scale byte that a block's four lanes agree on, lane j keeps that of rows
-// 4 q + j; two exchanges of bytes between lanes then give each lane the four bytes of one row (half-warp
-// a: atom a, lane n of it: row n), which leave as two runs of 64 bytes.  No shared memory and no
-// barriers but for the ragged groups' table: the warps' loads overlap freely.
+// Of the scale byte that a block's two lanes agree on, lane j of half h keeps those of rows
+// n = 4 q + 2 j + h (q = 0 .. 3); two exchanges of bytes between the lanes of b then give each lane the
+// four blocks' bytes of one row, which leave as runs of 64 bytes.  No shared memory and no barriers but
+// for the ragged groups' table.
+// Bound by memory: 16384 x 7168 bf16 takes 45 us, 6.5 TB/s of values read and codes written.  With 8
+// values a lane the instructions bound it (60 us): 16 halve the maxima's exchanges and the scales'
+// arithmetic for each value.
 // PAIRED: rows are the gate and linear projections of a SwiGLU interleaved in groups of 64 (row
 // 128 (j / 64) + j % 64 = w1[j], 64 further w3[j]).
-constexpr int kMx4Batch = 4;  // rows in flight a warp
 template <typename T, bool PAIRED>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) mx4_quant_kernel(const Mx4QuantParams p) {
+__global__ void __launch_bounds__(256, 4) mx4_quant_kernel(const Mx4QuantParams p) {
   __shared__ int table[kMx4TableInts];
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // rows in flight a half-warp
   pdl_wait();
   pdl_trigger();
   const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, half = lane >> 4;
   const unsigned nkb = (unsigned)mx4_kblocks(p.cols);
   const unsigned n = (unsigned)tiles.total * nkb * 8;  // less than 2^31, as the host has seen to
+  const long long pitch = p.cols >> 1;
+  const long long to3 = PAIRED ? static_cast<const T*>(p.src3) - static_cast<const T*>(p.src) : 0;
   for (unsigned u = blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += gridDim.x * 8) {
     const int sl = (int)(u & 7);
     const unsigned tk = u >> 3;
     const int t = (int)(tk / nkb), kb = (int)(tk - t * nkb);
     int g, row0, valid;
     tiles.get(t, g, row0, valid);
-    const int c = kb * 256 + lane * 8;
-    const bool in = c < p.cols;  // cols is a multiple of 32: a block is inside or outside whole
+    const int c = kb * 256 + (lane & 15) * 16;
+    // the slice's first row
+    const T* src;
+    if constexpr (PAIRED) {
+      // interleaved row -> row of w1 or w3 (group g has 2h rows): row n of a slice is one of w3's for
+      // n % 4 = 2, 3
+      const int within = row0 - g * tiles.group_rows;
+      src = static_cast<const T*>(p.src) + ((long long)g * (tiles.group_rows >> 1) + (within >> 1) + 4 * sl) * p.ld + c;
+    } else {
+      src = static_cast<const T*>(p.src) + (long long)(row0 + 4 * sl) * p.ld + c;
+    }
+    uint8_t* dst = p.elems + (long long)(row0 + 4 * sl) * pitch + (c >> 1);
+    // rows from the slice's first on that exist (cols is a multiple of 32: a block is inside or outside)
+    const int left = c < p.cols ? valid - 4 * sl : 0;
     uint32_t word = 0;
+    auto rows = [&](auto whole) {
 #pragma unroll
-    for (int b = 0; b < 16; b += kMx4Batch) {
-      Mx4Raw<T> raw[kMx4Batch];
+      for (int b = 0; b < 8; b += kBatch) {
+        Mx4Raw<T> raw[kBatch];
 #pragma unroll
-      for (int i = 0; i < kMx4Batch; ++i) {
-        const int r = mx4_slice_row(sl, b + i);
-#pragma unroll
-        for (int j = 0; j < (int)(2 * sizeof(T)); ++j) raw[i].w[j] = 0;
-        if (in && r < valid) {
-          const int row = row0 + r;
-          if constexpr (PAIRED) {
-            // row of the interleaved matrix -> row of w1 or w3 (group g has 2h rows)
-            const int within = row - g * tiles.group_rows;
-            const long long srow = (long long)g * (tiles.group_rows >> 1) + (within >> 7) * 64 + (within & 63);
-            mx4_load8(static_cast<const T*>((within & 64) ? p.src3 : p.src) + srow * p.ld + c, p.vec, raw[i]);
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = mx4_row(2 * (b + i)) + 32 * half;  // row 2 (b + i) + half of the slice
+          const long long at = PAIRED ? (long long)(r & 63) * p.ld + ((r & 64) ? to3 : 0) : (long long)r * p.ld;
+          if (decltype(whole)::value || r < left) {
+            mx4_load16(src + at, p.access, raw[i]);
           } else {
-            mx4_load8(static_cast<const T*>(p.src) + (long long)row * p.ld + c, p.vec, raw[i]);
+#pragma unroll
+            for (int j = 0; j < (int)(4 * sizeof(T)); ++j) raw[i].w[j] = 0;
           }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < kMx4Batch; ++i) {
-        const int r = mx4_slice_row(sl, b + i);
-        uint32_t amax = mx4_amax(raw[i]);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const uint32_t sb = mx4_scale_byte(amax);
-        // 2^-X = 2^(127 - byte): exponent field 254 - byte, at least 2 for every finite block
-        const float s = __uint_as_float((254u - min(sb, 252u)) << 23);
-        if (in && r < valid) {
-          float v[8];
-          mx4_floats(raw[i], v);
-          *reinterpret_cast<uint32_t*>(p.elems + (long long)(row0 + r) * (p.cols >> 1) + (c >> 1)) = e2m1x8(v, s);
+        for (int i = 0; i < kBatch; ++i) {
+          const int step = b + i, r = mx4_row(2 * step) + 32 * half;
+          const uint32_t ex = mx4_exponent(raw[i]);
+          // scale byte: the exponent field less 2, so that the largest value lands in [4, 8)
+          const uint32_t e = max(ex, 2u), sb = ex == 255u ? 255u : e - 2;
+          if (decltype(whole)::value || r < left) *reinterpret_cast<uint2*>(dst + r * pitch) = mx4_codes(raw[i], e);
+          if ((lane & 1) == (step & 1)) word |= sb << (8 * (step >> 1));
         }
-        if ((lane & 3) == ((b + i) & 3)) word |= sb << (8 * ((b + i) >> 2));
       }
-    }
-    // bytes (block (lane >> 2) & 3, q = 0 .. 3) -> (row 4 ((lane >> 2) & 3) + lane % 4, block = 0 .. 3)
-    uint32_t y = __shfl_xor_sync(0xffffffffu, word, 4);
-    word = __byte_perm(word, y, (lane & 4) ? 0x3715 : 0x6240);
-    y = __shfl_xor_sync(0xffffffffu, word, 8);
-    word = __byte_perm(word, y, (lane & 8) ? 0x3276 : 0x5410);
-    // row n of the slice: byte 16 (4 sl + n / 4) + 4 (n % 4) = 64 sl + 4 n of its atom
-    *reinterpret_cast<uint32_t*>(p.scales + (size_t)tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15)) = word;
+    };
+    if (__all_sync(0xffffffffu, left >= 100)) rows(std::true_type()); else rows(std::false_type());  // 99 = 3 + 96
+    // bytes (b, q = 0 .. 3) -> (q = b, blocks 0 .. 3)
+    uint32_t y = __shfl_xor_sync(0xffffffffu, word, 2);
+    word = __byte_perm(word, y, (lane & 2) ? 0x3715 : 0x6240);
+    y = __shfl_xor_sync(0xffffffffu, word, 4);
+    word = __byte_perm(word, y, (lane & 4) ? 0x3276 : 0x5410);
+    // row n = 4 b + 2 j + h: byte 64 sl + 4 n of atom a
+    const int row16 = 4 * ((lane >> 1) & 3) + 2 * (lane & 1) + half;
+    *reinterpret_cast<uint32_t*>(p.scales + (size_t)tk * 1024 + ((lane >> 3) & 1) * 512 + 64 * sl + 4 * row16) = word;
   }
 }
 
@@ -326,76 +361,105 @@ struct Mx4DequantParams {
   int cols;
   Mx4Rows rows;
   uint32_t* status;
-  int vec;
+  int access;        // Mx4Access of out
   int zero_rest;     // 1: rows of no group are set to zero
 };
 
 // The values of eight codes (the first in the lowest four bits) times s; fp16 holds every code's value.
-__device__ __forceinline__ void e2m1_values(uint32_t w, float s, float (&v)[8]) {
+__device__ __forceinline__ void e2m1_values(uint32_t w, float s, float* v) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * j)), __NV_E2M1);
-    const float2 f = __half22float2(__half2(h));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
     v[2 * j] = f.x * s;
     v[2 * j + 1] = f.y * s;
   }
 }
-
-// Same slices and lanes as the quantisation.
+// Sixteen values of a row.
 template <typename T>
-__global__ void __launch_bounds__(256, 5) mx4_dequant_kernel(const Mx4DequantParams p) {
+__device__ __forceinline__ void mx4_store16v(T* o, int access, const float (&v)[16]) {
+  uint32_t w[4 * sizeof(T)];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  }
+  if (access == MX4_32) {
+#pragma unroll
+    for (int i = 0; i < (int)(4 * sizeof(T)); i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(o) + i),
+                   "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                   "r"(w[i + 7])
+                   : "memory");
+  } else if (access == MX4_16) {
+#pragma unroll
+    for (int i = 0; i < (int)(4 * sizeof(T)); i += 4)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(o) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = from_f<T>(v[j]);
+  }
+}
+
+// Same slices and lanes as the quantisation.  16384 x 7168 to bf16: 49 us, 6.1 TB/s.
+template <typename T>
+__global__ void __launch_bounds__(256, 4) mx4_dequant_kernel(const Mx4DequantParams p) {
   __shared__ int table[kMx4TableInts];
   pdl_wait();
   pdl_trigger();
   const Mx4Tiles tiles = mx4_tiles(p.rows, table, p.status);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4;
   const unsigned nkb = (unsigned)mx4_kblocks(p.cols);
   const unsigned n = (unsigned)tiles.total * nkb * 8;
+  const long long pitch = p.cols >> 1;
   for (unsigned u = blockIdx.x * 8 + warp; u < n; u += gridDim.x * 8) {
     const int sl = (int)(u & 7);
     const unsigned tk = u >> 3;
     const int t = (int)(tk / nkb), kb = (int)(tk - t * nkb);
     int g, row0, valid;
     tiles.get(t, g, row0, valid);
-    const int c = kb * 256 + lane * 8;
-    const bool in = c < p.cols;
+    const int c = kb * 256 + (lane & 15) * 16;
+    const uint8_t* src = p.elems + (long long)(row0 + 4 * sl) * pitch + (c >> 1);
+    T* dst = static_cast<T*>(p.out) + (long long)(row0 + 4 * sl) * p.ld + c;
+    const int left = c < p.cols ? valid - 4 * sl : 0;
+    // lane 16 a + n: the four scale bytes of row n in atom a
     const uint32_t word =
         *reinterpret_cast<const uint32_t*>(p.scales + (size_t)tk * 1024 + (lane >> 4) * 512 + 64 * sl + 4 * (lane & 15));
-#pragma unroll 1
-    for (int b = 0; b < 16; b += 8) {
-      uint32_t w[8];
+    auto rows = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = mx4_slice_row(sl, b + i);
-        w[i] = 0;
-        if (in && r < valid)
-          w[i] = *reinterpret_cast<const uint32_t*>(p.elems + (long long)(row0 + r) * (p.cols >> 1) + (c >> 1));
-      }
+      for (int b = 0; b < 8; b += 4) {
+        uint2 w[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = mx4_slice_row(sl, b + i);
-        const uint32_t sb = (__shfl_sync(0xffffffffu, word, (lane & 16) + b + i) >> (8 * ((lane >> 2) & 3))) & 255u;
-        // 2^(byte - 127): a subnormal for byte 0, NaN for 255
-        const float s = sb == 255u ? __uint_as_float(0x7FC00000u)
-                                   : (sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u));
-        float v[8];
-        e2m1_values(w[i], s, v);
-        if (!in || r >= valid) continue;
-        T* o = static_cast<T*>(p.out) + (long long)(row0 + r) * p.ld + c;
-        if (p.vec) {
-          if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-          }
-        } else {
+        for (int i = 0; i < 4; ++i) {
+          const int r = mx4_row(2 * (b + i)) + 32 * half;
+          w[i] = decltype(whole)::value || r < left ? *reinterpret_cast<const uint2*>(src + r * pitch) : make_uint2(0, 0);
+        }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = from_f<T>(v[j]);
+        for (int i = 0; i < 4; ++i) {
+          const int step = b + i, r = mx4_row(2 * step) + 32 * half;
+          const uint32_t sw = __shfl_sync(0xffffffffu, word, ((lane << 1) & 16) + 2 * step + half);
+          const uint32_t sb = (sw >> (8 * ((lane >> 1) & 3))) & 255u;
+          // 2^(byte - 127); the extra bit makes byte 0 the subnormal 2^-127 and byte 255 a NaN
+          const float s = __uint_as_float((sb << 23) | (((sb + 1) & 0xFEu) ? 0u : 0x00400000u));
+          if (!decltype(whole)::value && r >= left) continue;
+          float v[16];
+          e2m1_values(w[i].x, s, v);
+          e2m1_values(w[i].y, s, v + 8);
+          mx4_store16v(dst + r * p.ld, p.access, v);
         }
       }
-    }
+    };
+    if (__all_sync(0xffffffffu, left >= 100)) rows(std::true_type()); else rows(std::false_type());
   }
   if (p.zero_rest)
     mx4_zero_rest(tiles, p.rows.rows, static_cast<T*>(p.out), p.ld, p.cols, blockIdx.x * 8 + warp, gridDim.x * 8, lane);

@@ -40,14 +40,15 @@ long long work_tiles(int64_t rows, int32_t groups, bool ragged) {
   return ragged ? rows / 128 + std::min<int64_t>(groups, rows) : scale_tiles(rows, groups, false);
 }
 
-template <typename T>
-bool rows16(const void* p, int64_t ld) {
-  return ((uintptr_t)p & 15) == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+// Widest access that every row of a matrix allows (rows `ld` elements apart).
+int row_access(const void* p, int64_t ld, int32_t dtype) {
+  const uint64_t a = (uint64_t)(uintptr_t)p | (uint64_t)(ld * (dtype == LMOE_F32 ? 4 : 2));
+  return a % 32 == 0 ? MX4_32 : (a % 16 == 0 ? MX4_16 : MX4_ELEMENTS);
 }
 
-// Persistent grid of the quantisation kernels (eight warps a block, a block a tile and k-block): at
-// most eight blocks an SM.
-int mx4_grid(long long tiles, int nkb, int sms) { return (int)std::min(tiles * nkb, 8ll * sms); }
+// Grid of the quantisation kernels (eight warps a block, a block a tile and k-block at a time): at most
+// 32 blocks an SM, so that what each does is even (eight cost dequantising a tenth more).
+int mx4_grid(long long tiles, int nkb, int sms) { return (int)std::min(tiles * nkb, 32ll * sms); }
 
 // Tensor map of a matrix's scale atoms: `tiles` row tiles of nkb k-blocks of 1 KB (two atoms), as rows of
 // 128 bytes; a box is one k-block of `box_tiles` row tiles.
@@ -95,14 +96,14 @@ struct Mx4Plan {
 Mx4Plan plan_mx4(int M, int N, int nkb, int groups, bool ragged, int sms) {
   const long long mt = work_tiles(M, groups, ragged);
   const long long t128 = mt * ((N + 127) / 128), t256 = mt * ((N + 255) / 256);
-  const int fs = getenv("MX4_SPLIT") ? atoi(getenv("MX4_SPLIT")) : 0;
-  if (fs) return {128, fs, (int)t128 * fs};
   // 256-wide tiles where they take fewer waves of the GPU by more than their longer k-blocks cost
   if ((t256 + sms - 1) / sms * 3 <= (t128 + sms - 1) / sms * 2)
     return {256, 1, (int)std::min<long long>(t256, sms)};
+  // too few tiles for the GPU and a long K: clusters share them (eight CTAs only while half the GPU
+  // holds them all, since not every SM has seven neighbours free)
   int split = 1;
   if (nkb >= 12)
-    while (split < 8 && nkb >= 8 * split && 2 * split * t128 <= sms) split *= 2;
+    while (split < 8 && nkb >= 8 * split && 2 * split * t128 <= (split < 4 ? sms : sms / 2)) split *= 2;
   return {128, split, (int)std::min<long long>(t128 * split, sms)};
 }
 
@@ -141,7 +142,7 @@ int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32
   p.elems = elems;
   p.scales = scales;
   p.status = status;
-  p.vec = dtype == LMOE_F32 ? rows16<float>(x, ld) : rows16<bf16>(x, ld);
+  p.access = row_access(x, ld, dtype);
   const int grid = mx4_grid(work_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
@@ -175,7 +176,7 @@ int lmoe_mx4_quant_w13(const void* w1, const void* w3, int32_t dtype, int32_t gr
   p.elems = elems;
   p.scales = scales;
   p.status = status;
-  p.vec = (((uintptr_t)w1 | (uintptr_t)w3) & 15) == 0;  // cols is a multiple of 32
+  p.access = std::min(row_access(w1, cols, dtype), row_access(w3, cols, dtype));
   const int grid = mx4_grid(work_tiles(rows, groups, false), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
@@ -208,7 +209,7 @@ int lmoe_mx4_dequant(const uint8_t* elems, const uint8_t* scales, int64_t rows, 
   p.rows = Mx4Rows{offsets, groups, (int)rows};
   p.status = status;
   p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
-  p.vec = dtype == LMOE_F32 ? rows16<float>(out, ld) : rows16<bf16>(out, ld);
+  p.access = row_access(out, ld, dtype);
   const int grid = mx4_grid(work_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
@@ -257,7 +258,7 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   p.ldc = ldc;
   p.c_cols = cols;
   p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
-  p.vec = c_dtype == LMOE_F32 ? rows16<float>(c, ldc) : rows16<bf16>(c, ldc);
+  p.vec = row_access(c, ldc, c_dtype) != MX4_ELEMENTS;
   p.status = status;
   if (p.vec && !make_map_c(&p.tmC, c, M, cols, ldc, c_dtype == LMOE_F32, swiglu ? 16 : 32)) return LMOE_ECUDA;
   cudaStream_t st = (cudaStream_t)stream;
