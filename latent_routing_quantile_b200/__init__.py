@@ -7,6 +7,7 @@ import of the binding still works, but the first call raises: there is no CPU fa
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, c_float, c_int, c_int32, c_size_t, c_uint32, c_void_p
 
@@ -461,6 +462,7 @@ def route_noalloc(scores, bias, k, out=None, stream=None):
 # Small calls last a few microseconds on the GPU, so their host side is kept short: plain integers to
 # ctypes, sizes worked out here, one look at the current device and stream.
 _status_words = {}  # device index -> (tensor, address)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
@@ -551,17 +553,29 @@ class Mx4:
     of three dimensions [groups, rows / groups, cols].  `glu`: gate and linear rows interleaved by
     mx4_quant_w13."""
 
-    __slots__ = ("elems", "scales", "rows", "cols", "groups", "offsets", "stacked", "glu")
+    __slots__ = ("buf", "rows", "cols", "groups", "offsets", "stacked", "glu", "_scales_at")
 
-    def __init__(self, rows, cols, groups, offsets, stacked, device, glu=False):
+    def __init__(self, rows, cols, groups, offsets, stacked, like, glu=False):
         if cols % 32 or cols == 0:
             raise LmoeError(f"columns must be a positive multiple of 32, got {cols}")
         self.rows, self.cols, self.groups, self.offsets = rows, cols, groups, offsets
         self.stacked, self.glu = stacked, glu
-        # the sizes of lmoe_mx4_bytes
+        # one buffer: the scales (the sizes of lmoe_mx4_bytes; a multiple of 1024 bytes), the elements
         tiles = (rows // groups + 127) // 128 * groups if offsets is None else (rows + 127) // 128 + groups
-        self.elems = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
-        self.scales = torch.empty(tiles * ((cols + 255) // 256) * 1024, dtype=torch.uint8, device=device)
+        self._scales_at = tiles * ((cols + 255) // 256) * 1024
+        self.buf = torch.empty(self._scales_at + rows * (cols // 2), dtype=torch.uint8, device=like.device)
+
+    @property
+    def scales(self):
+        return self.buf[:self._scales_at]
+
+    @property
+    def elems(self):
+        return self.buf[self._scales_at:].view(self.rows, self.cols // 2)
+
+    def _ptrs(self):
+        p = self.buf.data_ptr()
+        return p + self._scales_at, p
 
     def _match(self, rows, cols, groups, offsets, stacked, glu):
         if (self.rows, self.cols, self.groups, self.stacked, self.glu) != (rows, cols, groups, stacked, glu) or \
@@ -595,18 +609,19 @@ def mx4_quant(x, offsets=None, out=None, stream=None) -> Mx4:
         rows, cols, ld = groups * shape[1], shape[2], shape[2]
     else:
         raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets")
-    kept = (x, offsets) if out is None else (x, offsets, out.elems, out.scales)
-    dev = _device_of(*kept)
-    if stream is not None or dev != torch.cuda.current_device():
-        with _Elsewhere(dev, stream, *kept):
+    dev = _device_of(x, offsets, None if out is None else out.buf)
+    if stream is not None or dev != _current_device():
+        with _Elsewhere(dev, stream, x, offsets, None if out is None else out.buf):
             return mx4_quant(x, offsets, out)
     if out is None:
-        out = Mx4(rows, cols, groups, offsets, stacked, x.device)
+        out = Mx4(rows, cols, groups, offsets, stacked, x)
     else:
         out._match(rows, cols, groups, offsets, stacked, False)
-    _check(lib().lmoe_mx4_quant(x.data_ptr(), dt, ld, rows, cols, groups,
-                                None if offsets is None else offsets.data_ptr(), out.elems.data_ptr(),
-                                out.scales.data_ptr(), _status_word(dev), _raw_stream(dev)), "lmoe_mx4_quant")
+    elems, scales = out._ptrs()
+    rc = lib().lmoe_mx4_quant(x.data_ptr(), dt, ld, rows, cols, groups, None if offsets is None else offsets.data_ptr(),
+                              elems, scales, _status_word(dev), _raw_stream(dev))
+    if rc:
+        _check(rc, "lmoe_mx4_quant")
     return out
 
 
@@ -621,17 +636,17 @@ def mx4_quant_w13(w1, w3, out=None, stream=None) -> Mx4:
     stacked = w1.dim() == 3
     groups = w1.shape[0] if stacked else 1
     h, cols = w1.shape[-2:]
-    kept = (w1, w3) if out is None else (w1, w3, out.elems, out.scales)
-    dev = _device_of(*kept)
-    if stream is not None or dev != torch.cuda.current_device():
-        with _Elsewhere(dev, stream, *kept):
+    dev = _device_of(w1, w3, None if out is None else out.buf)
+    if stream is not None or dev != _current_device():
+        with _Elsewhere(dev, stream, w1, w3, None if out is None else out.buf):
             return mx4_quant_w13(w1, w3, out)
     if out is None:
-        out = Mx4(2 * groups * h, cols, groups, None, stacked, w1.device, glu=True)
+        out = Mx4(2 * groups * h, cols, groups, None, stacked, w1, glu=True)
     else:
         out._match(2 * groups * h, cols, groups, None, stacked, True)
-    _check(lib().lmoe_mx4_quant_w13(w1.data_ptr(), w3.data_ptr(), dt, groups, h, cols, out.elems.data_ptr(),
-                                    out.scales.data_ptr(), _status_word(dev), _raw_stream(dev)), "lmoe_mx4_quant_w13")
+    elems, scales = out._ptrs()
+    _check(lib().lmoe_mx4_quant_w13(w1.data_ptr(), w3.data_ptr(), dt, groups, h, cols, elems, scales,
+                                    _status_word(dev), _raw_stream(dev)), "lmoe_mx4_quant_w13")
     return out
 
 
@@ -642,17 +657,19 @@ def mx4_dequant(q: Mx4, dtype=torch.bfloat16, out=None, stream=None):
     shape = (q.groups, q.rows // q.groups, q.cols) if q.stacked else (q.rows, q.cols)
     if out is not None and (tuple(out.shape) != shape or not out.is_contiguous()):
         raise LmoeError(f"out must be contiguous and have shape {shape}")
-    kept = (q.elems, q.scales, q.offsets, out)
-    dev = _device_of(*kept)
-    if stream is not None or dev != torch.cuda.current_device():
-        with _Elsewhere(dev, stream, *kept):
+    offsets = q.offsets
+    dev = _device_of(q.buf, offsets, out)
+    if stream is not None or dev != _current_device():
+        with _Elsewhere(dev, stream, q.buf, offsets, out):
             return mx4_dequant(q, dtype, out)
     flags = 0
     if out is None:
-        out, flags = torch.empty(shape, dtype=dtype, device=q.elems.device), MX4_ZERO_REST
-    _check(lib().lmoe_mx4_dequant(q.elems.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, q.groups,
-                                  None if q.offsets is None else q.offsets.data_ptr(), out.data_ptr(), dt, q.cols,
-                                  flags, _status_word(dev), _raw_stream(dev)), "lmoe_mx4_dequant")
+        out, flags = torch.empty(shape, dtype=dtype, device=q.buf.device), MX4_ZERO_REST
+    elems, scales = q._ptrs()
+    rc = lib().lmoe_mx4_dequant(elems, scales, q.rows, q.cols, q.groups, None if offsets is None else offsets.data_ptr(),
+                                out.data_ptr(), dt, q.cols, flags, _status_word(dev), _raw_stream(dev))
+    if rc:
+        _check(rc, "lmoe_mx4_dequant")
     return out
 
 
@@ -665,7 +682,8 @@ def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, strea
         raise LmoeError("a must be one matrix of rows")
     if a.cols != b.cols:
         raise LmoeError(f"a and b disagree on K ({a.cols} and {b.cols})")
-    if b.offsets is not None or (a.offsets is None) == b.stacked or a.groups != b.groups:
+    offsets = a.offsets
+    if b.offsets is not None or (offsets is None) == b.stacked or a.groups != b.groups:
         raise LmoeError("a product takes a plain matrix b, or a with offsets and as many stacked matrices b")
     if bool(swiglu) != b.glu:
         raise LmoeError("swiglu=True goes with a matrix from mx4_quant_w13")
@@ -675,24 +693,31 @@ def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, strea
     if out is not None and (tuple(out.shape) != (M, cols) or (cols > 1 and out.stride(1) != 1) or
                             (M > 1 and out.stride(0) < cols)):
         raise LmoeError(f"out must have shape {(M, cols)}, contiguous columns and rows that do not overlap")
-    kept = (a.elems, a.scales, a.offsets, b.elems, b.scales, out)
-    dev = _device_of(*kept)
-    if stream is not None or dev != torch.cuda.current_device():
-        with _Elsewhere(dev, stream, *kept):
+    dev = _device_of(a.buf, offsets, b.buf, out)
+    if stream is not None or dev != _current_device():
+        with _Elsewhere(dev, stream, a.buf, offsets, b.buf, out):
             return mx4_gemm(a, b, swiglu, dtype, out)
     flags = MX4_SWIGLU if swiglu else 0
     ld = cols
     if out is None:
-        out, flags = torch.empty((M, cols), dtype=dtype, device=a.elems.device), flags | MX4_ZERO_REST
+        out, flags = torch.empty((M, cols), dtype=dtype, device=a.buf.device), flags | MX4_ZERO_REST
     elif M > 1:
         ld = out.stride(0)
-    _check(lib().lmoe_mx4_gemm(a.elems.data_ptr(), a.scales.data_ptr(), b.elems.data_ptr(), b.scales.data_ptr(), M, N,
-                               a.cols, a.groups, None if a.offsets is None else a.offsets.data_ptr(), out.data_ptr(),
-                               dt, ld, flags, _status_word(dev), _raw_stream(dev)), "lmoe_mx4_gemm")
+    ae, asc = a._ptrs()
+    be, bsc = b._ptrs()
+    rc = lib().lmoe_mx4_gemm(ae, asc, be, bsc, M, N, a.cols, a.groups, None if offsets is None else offsets.data_ptr(),
+                             out.data_ptr(), dt, ld, flags, _status_word(dev), _raw_stream(dev))
+    if rc:
+        _check(rc, "lmoe_mx4_gemm")
     return out
 
 
-_balance_scratch = 0
+@functools.lru_cache(None)
+def _balance_floats() -> int:
+    """fp32 values that hold a call's loss (the first 64 bytes) and scratch."""
+    n = c_size_t(0)
+    _check(lib().lmoe_balance_scratch_bytes(ctypes.byref(n)), "lmoe_balance_scratch_bytes")
+    return 16 + (n.value + 3) // 4
 
 
 def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream=None):
@@ -700,38 +725,48 @@ def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream
     as Layer.routing() gives them; cu_seqlens (int32 [S + 1]) bounds the sequences (None: one).
     Returns dict(loss [1] fp32, counts [S, E] int32, dscores [T, E] fp32): the gradient of the loss
     in the scores, left out with grad=False.  `out` may pass preallocated buffers."""
-    global _balance_scratch
     if scores.dim() != 2 or idx.dim() != 2:
         raise LmoeError("scores must be [T, E] and idx [T, k]")
     T, E = scores.shape
     k = idx.shape[1]
+    S = 1
+    if cu_seqlens is not None:
+        S = _offsets(cu_seqlens, "cu_seqlens").numel() - 1
     dev = _device_of(scores, idx, cu_seqlens)
     _dev(scores, torch.float32, None, "scores")
     _dev(idx, torch.int32, (T, k), "idx")
-    S = 1 if cu_seqlens is None else _offsets(cu_seqlens, "cu_seqlens").numel() - 1
     given = () if out is None else tuple(out.values())
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _Elsewhere(dev, stream, scores, idx, cu_seqlens, *given):
             return balance_loss(scores, idx, coef, cu_seqlens, grad, out)
-    _device_of(scores, *given)
-    if not _balance_scratch:
-        n = c_size_t(0)
-        _check(lib().lmoe_balance_scratch_bytes(ctypes.byref(n)), "lmoe_balance_scratch_bytes")
-        _balance_scratch = n.value
-    out = dict(out or ())
-    shapes = (("loss", (1,), torch.float32), ("counts", (S, E), torch.int32), ("dscores", (T, E), torch.float32))
-    for name, shape, dt in shapes if grad else shapes[:2]:
-        if name in out:
-            _dev(out[name], dt, shape, name)
+    if given:
+        _device_of(scores, *given)
+    device = scores.device
+    # the loss and the call's scratch share a buffer
+    buf = torch.empty(_balance_floats(), dtype=torch.float32, device=device)
+    res = dict(out or ())
+    if "loss" in res:
+        _dev(res["loss"], torch.float32, (1,), "loss")
+    else:
+        res["loss"] = buf[:1]
+    if "counts" in res:
+        _dev(res["counts"], torch.int32, (S, E), "counts")
+    else:
+        res["counts"] = torch.empty((S, E), dtype=torch.int32, device=device)
+    dscores = None
+    if grad:
+        if "dscores" in res:
+            _dev(res["dscores"], torch.float32, (T, E), "dscores")
         else:
-            out[name] = torch.empty(shape, dtype=dt, device=scores.device)
-    scratch = torch.empty(_balance_scratch, dtype=torch.uint8, device=scores.device)
-    _check(lib().lmoe_balance_loss(scores.data_ptr(), idx.data_ptr(), T, E, k,
-                                   None if cu_seqlens is None else cu_seqlens.data_ptr(), S, float(coef),
-                                   out["counts"].data_ptr(), out["loss"].data_ptr(),
-                                   out["dscores"].data_ptr() if grad else None, scratch.data_ptr(),
-                                   _status_word(dev), _raw_stream(dev)), "lmoe_balance_loss")
-    return out
+            res["dscores"] = torch.empty_like(scores)
+        dscores = res["dscores"].data_ptr()
+    rc = lib().lmoe_balance_loss(scores.data_ptr(), idx.data_ptr(), T, E, k,
+                                 None if cu_seqlens is None else cu_seqlens.data_ptr(), S, coef,
+                                 res["counts"].data_ptr(), res["loss"].data_ptr(), dscores, buf.data_ptr() + 64,
+                                 _status_word(dev), _raw_stream(dev))
+    if rc:
+        _check(rc, "lmoe_balance_loss")
+    return res
 
 
 def layer_from_weights(shape, weights_cpu: dict, max_tokens=None, device="cuda", stream=None,
