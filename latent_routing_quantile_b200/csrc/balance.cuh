@@ -7,16 +7,23 @@
 //   L    = coef / S' sum_q sum_e f_qe mean_{t in q} p_te  =  sum_t w_q D_t
 // The choice is piecewise constant, so f has no gradient, and
 //   dL/ds_te = w_q (f_qe - D_t) / R_t.
-// With the counts known, the loss and its gradient need one pass over the scores, a warp a token: the
-// mean probabilities are never formed.  It is bound by that pass (scores read, gradient written).
+// With the counts known, the loss and its gradient need one pass over the scores: the mean
+// probabilities are never formed.  The pass is bound by memory (scores read, gradient written).
+//
+// Two forms.  A batch whose scores a few SMs can stream takes one launch of one cluster of CTAs, which
+// count their own tokens, add the counts up through distributed shared memory and go on to the pass.
+// A larger one takes two launches over the whole GPU, counting (integer atomics: their order does not
+// matter) and the pass.  Either way the loss's partial sums are added in a fixed order, in 64 bits.
 #pragma once
 
 #include "common.cuh"
 
 namespace lmoe {
 
-constexpr int kBalThreads = 256;
-constexpr int kBalMaxBlocks = 2048;
+constexpr int kBalThreads = 512;
+constexpr int kBalMaxBlocks = 1024;
+constexpr int kBalHistInts = 8192;   // shared counters of a block
+constexpr int kBalMaxCluster = 16;
 
 struct BalanceParams {
   const float* scores;   // [T, E]
@@ -33,159 +40,307 @@ struct BalanceParams {
   int chunk;             // tokens a block
 };
 
-__device__ __forceinline__ int bal_cu(const BalanceParams& p, int q) {
-  return p.cu ? min(max(p.cu[q], 0), p.T) : (q ? p.T : 0);
-}
-// The last sequence that begins at or before token t (-1: none does).
-__device__ __forceinline__ int bal_seq(const BalanceParams& p, int t) {
-  int lo = -1, hi = p.S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (bal_cu(p, mid) <= t) lo = mid; else hi = mid;
+// Sequence bounds a block needs, checked: cu that decreases or leaves [0, T] is reported and counts as
+// no sequence at all.  Up to kBalSeqCache sequences' bounds are kept in shared memory, where looking a
+// token's sequence up does not wait for memory step by step.
+constexpr int kBalSeqCache = 1023;
+struct BalSeqs {
+  const int* cu;   // shared or global
+  int S, filled;
+  __device__ __forceinline__ int begin(int q) const { return cu[q]; }
+  // The last sequence that begins at or before token t (-1: none does).
+  __device__ __forceinline__ int at(int t) const {
+    int lo = -1, hi = S;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (begin(mid) <= t) lo = mid; else hi = mid;
+    }
+    return lo;
   }
-  return lo;
+};
+struct BalSeqSmem {
+  int cu[kBalSeqCache + 1];
+  int filled, bad;
+};
+// The whole block takes part.
+__device__ __forceinline__ BalSeqs bal_seqs(const BalanceParams& p, BalSeqSmem& m) {
+  if (threadIdx.x == 0) m.filled = m.bad = 0;
+  __syncthreads();
+  int mine = 0, bad = 0;
+  for (int q = threadIdx.x; q < p.S; q += kBalThreads) {
+    const int a = p.cu ? p.cu[q] : 0, b = p.cu ? p.cu[q + 1] : p.T;
+    mine += b > a;
+    bad |= a < 0 || b > p.T || b < a;
+    if (p.S <= kBalSeqCache) {
+      m.cu[q] = a;
+      if (q == p.S - 1) m.cu[p.S] = b;
+    }
+  }
+  if (mine) atomicAdd(&m.filled, mine);
+  if (bad) m.bad = 1;
+  __syncthreads();
+  if (m.bad && threadIdx.x == 0) set_status(p.status, LMOE_STATUS_BAD_INDEX);
+  return BalSeqs{p.S <= kBalSeqCache ? m.cu : p.cu, m.bad ? 0 : p.S, m.filled};
 }
 
-// counts: a block counts a run of tokens in shared memory, sequence by sequence, and adds what it
-// found (integer atomics: the order does not matter).
-__global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const BalanceParams p) {
-  extern __shared__ int hist[];
-  pdl_wait();
-  pdl_trigger();
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) *p.done = 0;
-    if (p.cu)
-      for (int q = threadIdx.x; q <= p.S; q += kBalThreads)
-        if (p.cu[q] < 0 || p.cu[q] > p.T || (q && p.cu[q] < p.cu[q - 1])) set_status(p.status, LMOE_STATUS_BAD_INDEX);
-  }
-  for (int q = max(bal_seq(p, t0), 0); q < p.S; ++q) {
-    const int lo = max(t0, bal_cu(p, q)), hi = min(t1, bal_cu(p, q + 1));
-    if (bal_cu(p, q) >= t1) break;
-    if (lo >= hi) continue;
-    for (int e = threadIdx.x; e < p.E; e += kBalThreads) hist[e] = 0;
-    __syncthreads();
-    for (long long i = (long long)lo * p.k + threadIdx.x; i < (long long)hi * p.k; i += kBalThreads) {
-      const int e = p.idx[i];
-      if ((unsigned)e < (unsigned)p.E) atomicAdd(&hist[e], 1);
-      else if (e != -1) set_status(p.status, LMOE_STATUS_BAD_INDEX);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kBalThreads)
-      if (hist[e]) atomicAdd(&p.counts[(long long)q * p.E + e], hist[e]);
-    __syncthreads();
+// Copies of each of n shared counters: a power of two up to 32, one a lane where there is room, so that
+// few experts' counters do not make the lanes wait for each other.
+__device__ __forceinline__ int bal_copies(int n) {
+  int c = 32;
+  while (c > 1 && n * c > kBalHistInts) c >>= 1;
+  return c;
+}
+// Adds the choices of tokens [lo, hi) to hist (copies of each expert side by side).
+__device__ __forceinline__ void bal_count(const BalanceParams& p, int lo, int hi, int* hist, int copies) {
+  const int mine = threadIdx.x & (copies - 1);
+  const int end = hi * p.k;  // T k is at most 2^30
+#pragma unroll 4
+  for (int i = lo * p.k + threadIdx.x; i < end; i += kBalThreads) {
+    const int e = p.idx[i];
+    if ((unsigned)e < (unsigned)p.E) atomicAdd(&hist[e * copies + mine], 1);
+    else if (e != -1) set_status(p.status, LMOE_STATUS_BAD_INDEX);
   }
 }
 
-// loss and gradient, a warp a token; lane l holds experts VEC (l + 32 j) .. + VEC - 1.
-template <int NJ, int VEC>
-__global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalanceParams p) {
-  __shared__ float wsum[kBalThreads / 32];
-  __shared__ int filled;
-  __shared__ bool last;
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) filled = 0;
-  __syncthreads();
-  int mine = 0;
-  for (int q = threadIdx.x; q < p.S; q += kBalThreads) mine += bal_cu(p, q + 1) > bal_cu(p, q);
-  if (mine) atomicAdd(&filled, mine);
-  __syncthreads();
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-  float f[NJ * VEC];
-  float acc = 0.f, wq = 0.f;
-  int q_lo = 0, q_hi = 0;  // token range for which f and wq hold
-  bool inside = false, nan = false;
-  for (int t = t0 + warp; t < t1; t += kBalThreads / 32) {
-    if (t >= q_hi || t < q_lo) {
-      const int q = bal_seq(p, t);
-      inside = q >= 0 && t < bal_cu(p, q + 1);
-      q_lo = t;
-      q_hi = t + 1;
-      if (inside) {
-        q_hi = bal_cu(p, q + 1);
-        const int n = q_hi - bal_cu(p, q);
-        const float fs = (float)p.E / ((float)p.k * (float)n);
-        wq = p.coef / ((float)filled * (float)n);
+// The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe.  LANES lanes share a row (a warp
+// takes 32 / LANES rows side by side) and R such sets of rows are in flight; lane l of a row holds experts
+// VEC (l + LANES j) .. + VEC - 1.  Returns the lane's sum of D (lane 0 of each row's); nan: some score
+// was a NaN.
+template <int NJ, int VEC, int R, int LANES>
+__device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
+  constexpr int kSide = 32 / LANES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LANES - 1), side = (threadIdx.x & 31) / LANES;
+  float acc = 0.f;
+  for (int t0 = lo + warp * R * kSide + side; t0 - side < hi; t0 += kBalThreads / 32 * R * kSide) {
+    float s[R][NJ * VEC], sum[R], dot[R];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const int e = (lane + 32 * j) * VEC + i;
-            f[j * VEC + i] = e < p.E ? (float)p.counts[(long long)q * p.E + e] * fs : 0.f;
-          }
-      }
-    }
-    const float* srow = p.scores + (long long)t * p.E;
-    float* drow = p.dscores ? p.dscores + (long long)t * p.E : nullptr;
-    float s[NJ * VEC];
-    float R = 0.f, D = 0.f;
-    if (inside) {
+    for (int r = 0; r < R; ++r) {
+      const float* srow = p.scores + (long long)min(t0 + r * kSide, hi - 1) * p.E;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int e = (lane + 32 * j) * VEC;
+        const int e = (lane + LANES * j) * VEC;
         if constexpr (VEC == 4) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (e < p.E) v = __ldcs(reinterpret_cast<const float4*>(srow + e));
-          s[4 * j] = v.x; s[4 * j + 1] = v.y; s[4 * j + 2] = v.z; s[4 * j + 3] = v.w;
+          s[r][4 * j] = v.x; s[r][4 * j + 1] = v.y; s[r][4 * j + 2] = v.z; s[r][4 * j + 3] = v.w;
         } else {
-          s[j] = e < p.E ? __ldcs(srow + e) : 0.f;
+          s[r][j] = e < p.E ? __ldcs(srow + e) : 0.f;
         }
       }
-#pragma unroll
-      for (int i = 0; i < NJ * VEC; ++i) {
-        R += s[i];
-        D = fmaf(s[i], f[i], D);
-      }
-#pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        R += __shfl_xor_sync(0xffffffffu, R, off);
-        D += __shfl_xor_sync(0xffffffffu, D, off);
-      }
-      nan |= R != R;
     }
-    // a row of zeros has no probabilities: it adds nothing and gets no gradient
-    const float inv = inside && R != 0.f ? 1.f / R : 0.f;
-    D *= inv;
-    const float g = wq * inv;
-    if (inside) acc = fmaf(wq, D, acc);
-    if (drow) {
+    auto fval = [&](int j) {
+      const int e = (lane + LANES * j) * VEC;
+      if constexpr (VEC == 4) return e < p.E ? *reinterpret_cast<const float4*>(f + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      else return make_float4(e < p.E ? f[e] : 0.f, 0.f, 0.f, 0.f);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) sum[r] = dot[r] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const float4 fv = fval(j);
+      const float fe[4] = {fv.x, fv.y, fv.z, fv.w};
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          sum[r] += s[r][j * VEC + i];
+          dot[r] = fmaf(s[r][j * VEC + i], fe[i], dot[r]);
+        }
+    }
+#pragma unroll
+    for (int off = LANES / 2; off; off >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], off);
+        dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], off);
+      }
+    float g[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // a row of zeros has no probabilities: it adds nothing and gets no gradient
+      const float inv = sum[r] != 0.f ? 1.f / sum[r] : 0.f;
+      dot[r] *= inv;
+      g[r] = wq * inv;
+      if (t0 + r * kSide < hi) {
+        if (lane == 0) acc += dot[r];
+        nan |= sum[r] != sum[r];
+      }
+    }
+    if (p.dscores) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int e = (lane + 32 * j) * VEC;
+        const int e = (lane + LANES * j) * VEC;
         if (e >= p.E) continue;
-        if constexpr (VEC == 4) {
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (inside)
-            o = make_float4(g * (f[4 * j] - D), g * (f[4 * j + 1] - D), g * (f[4 * j + 2] - D), g * (f[4 * j + 3] - D));
-          *reinterpret_cast<float4*>(drow + e) = o;
-        } else {
-          drow[e] = inside ? g * (f[j] - D) : 0.f;
+        const float4 fv = fval(j);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (t0 + r * kSide >= hi) continue;
+          float* d = p.dscores + (long long)(t0 + r * kSide) * p.E + e;
+          if constexpr (VEC == 4)
+            *reinterpret_cast<float4*>(d) = make_float4(g[r] * (fv.x - dot[r]), g[r] * (fv.y - dot[r]),
+                                                        g[r] * (fv.z - dot[r]), g[r] * (fv.w - dot[r]));
+          else
+            *d = g[r] * (fv.x - dot[r]);
         }
       }
     }
   }
-  if (nan && lane == 0) set_status(p.status, LMOE_STATUS_NAN_SCORE);
-  // the blocks' sums are added in their order by the last block to finish, in 64 bits
+  return acc;
+}
+
+// The pass over tokens [t0, t1), sequence by sequence (counts known): the block's share of the loss, for
+// thread 0.  f: shared, [E]; wsum: shared, [kBalThreads / 32] doubles.
+template <int NJ, int VEC, int R, int LANES>
+__device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs& sq, int t0, int t1, float* f, double* wsum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  double acc = 0;
+  bool nan = false;
+  // tokens before the first sequence and behind the last
+  if (p.dscores) {
+    const int first = sq.S ? sq.begin(0) : p.T, end = sq.S ? sq.begin(sq.S) : p.T;
+    const long long a1 = (long long)min(t1, first) * p.E, b0 = (long long)max(t0, end) * p.E, b1 = (long long)t1 * p.E;
+    for (long long i = (long long)t0 * p.E + threadIdx.x; i < a1; i += kBalThreads) p.dscores[i] = 0.f;
+    for (long long i = b0 + threadIdx.x; i < b1; i += kBalThreads) p.dscores[i] = 0.f;
+  }
+  for (int q = max(sq.at(t0), 0); q < sq.S; ++q) {
+    const int b = sq.begin(q), e = sq.begin(q + 1);
+    if (b >= t1) break;
+    if (max(b, t0) >= min(e, t1)) continue;
+    const float n = (float)(e - b), fs = (float)p.E / ((float)p.k * n), wq = p.coef / ((float)sq.filled * n);
+    __syncthreads();  // the sequence before is done with f
+    for (int i = threadIdx.x; i < p.E; i += kBalThreads) f[i] = (float)p.counts[(long long)q * p.E + i] * fs;
+    __syncthreads();
+    acc += (double)wq * bal_rows<NJ, VEC, R, LANES>(p, max(b, t0), min(e, t1), f, wq, nan);
+  }
+  if (__any_sync(0xffffffffu, nan) && lane == 0) set_status(p.status, LMOE_STATUS_NAN_SCORE);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (lane == 0) wsum[warp] = acc;
   __syncthreads();
+  double sum = 0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kBalThreads / 32; ++w) sum += wsum[w];
+  return sum;
+}
+
+// Counts of the second form: a block counts a run of tokens, sequence by sequence.
+__global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const BalanceParams p) {
+  __shared__ int hist[kBalHistInts];
+  __shared__ BalSeqSmem seqs;
+  pdl_wait();
+  pdl_trigger();
+  const BalSeqs sq = bal_seqs(p, seqs);
+  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+  const int copies = bal_copies(p.E);
+  for (int q = max(sq.at(t0), 0); q < sq.S; ++q) {
+    const int b = sq.begin(q), lo = max(t0, b), hi = min(t1, sq.begin(q + 1));
+    if (b >= t1) break;
+    if (lo >= hi) continue;
+    for (int i = threadIdx.x; i < p.E * copies; i += kBalThreads) hist[i] = 0;
+    __syncthreads();
+    bal_count(p, lo, hi, hist, copies);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kBalThreads) {
+      int c = 0;
+      for (int i = 0; i < copies; ++i) c += hist[e * copies + ((i + e) & (copies - 1))];
+      if (c) atomicAdd(&p.counts[(long long)q * p.E + e], c);
+    }
+    __syncthreads();
+  }
+}
+
+// The pass of the second form.
+template <int NJ, int VEC, int R, int LANES>
+__global__ void __launch_bounds__(kBalThreads, 2) balance_kernel(const BalanceParams p) {
+  __shared__ __align__(16) float f[1024];
+  __shared__ double wsum[kBalThreads / 32];
+  __shared__ BalSeqSmem seqs;
+  __shared__ bool last;
+  pdl_wait();
+  pdl_trigger();
+  const BalSeqs sq = bal_seqs(p, seqs);
+  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
+  const double sum = bal_pass<NJ, VEC, R, LANES>(p, sq, t0, t1, f, wsum);
+  // the blocks' sums are added in their order by the last block to finish
   if (threadIdx.x == 0) {
-    double b = 0;
-    for (int w = 0; w < kBalThreads / 32; ++w) b += wsum[w];
-    p.partial[blockIdx.x] = b;
+    p.partial[blockIdx.x] = sum;
     __threadfence();
     last = atomicAdd(p.done, 1u) == gridDim.x - 1;
   }
   __syncthreads();
-  if (last && warp == 0) {
+  if (last && threadIdx.x < 32) {
     __threadfence();
     double b = 0;
-    for (int i = lane; i < (int)gridDim.x; i += 32) b += reinterpret_cast<volatile double*>(p.partial)[i];
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += 32) b += reinterpret_cast<volatile double*>(p.partial)[i];
 #pragma unroll
     for (int off = 16; off; off >>= 1) b += __shfl_xor_sync(0xffffffffu, b, off);
-    if (lane == 0) *p.loss = (float)b;
+    if (threadIdx.x == 0) *p.loss = (float)b;
   }
+}
+
+// The first form: one cluster, S E at most kBalHistInts.
+__device__ __forceinline__ int ld_cluster_int(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)));
+  return v;
+}
+__device__ __forceinline__ double ld_cluster_double(const double* p, uint32_t rank) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(smem_u32(p), rank)));
+  return v;
+}
+template <int NJ, int VEC, int R, int LANES>
+__global__ void __launch_bounds__(kBalThreads) balance_cluster_kernel(const BalanceParams p) {
+  __shared__ int hist[kBalHistInts];
+  __shared__ __align__(16) float f[1024];
+  __shared__ double wsum[kBalThreads / 32], total;
+  __shared__ BalSeqSmem seqs;
+  pdl_wait();
+  pdl_trigger();
+  const int n = p.S * p.E, copies = bal_copies(n), ctas = gridDim.x, rank = blockIdx.x;
+  for (int i = threadIdx.x; i < n * copies; i += kBalThreads) hist[i] = 0;
+  const BalSeqs sq = bal_seqs(p, seqs);  // ends with a barrier
+  const int t0 = min(p.T, rank * p.chunk), t1 = min(p.T, t0 + p.chunk);
+  if (t0 < t1)
+    for (int q = max(sq.at(t0), 0); q < sq.S; ++q) {
+      const int b = sq.begin(q), lo = max(t0, b), hi = min(t1, sq.begin(q + 1));
+      if (b >= t1) break;
+      if (lo < hi) bal_count(p, lo, hi, hist + q * p.E * copies, copies);
+    }
+  __syncthreads();
+  // each counter's copies into the first
+  if (copies > 1) {
+    for (int i = threadIdx.x; i < n; i += kBalThreads) {
+      int c = 0;
+      for (int j = 0; j < copies; ++j) c += hist[i * copies + ((j + i) & (copies - 1))];
+      hist[i * copies] = c;
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();
+  for (int i = rank * kBalThreads + threadIdx.x; i < n; i += ctas * kBalThreads) {
+    int c[kBalMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kBalMaxCluster; ++r) c[r] = r < ctas ? ld_cluster_int(&hist[i * copies], r) : 0;
+    int sum = 0;
+#pragma unroll
+    for (int r = 0; r < kBalMaxCluster; ++r) sum += c[r];
+    p.counts[i] = sum;
+  }
+  __syncthreads();
+  cluster_sync_all();  // every CTA sees the counts
+  const double sum = bal_pass<NJ, VEC, R, LANES>(p, sq, t0, t1, f, wsum);
+  if (threadIdx.x == 0) total = sum;
+  __syncthreads();
+  cluster_sync_all();
+  if (rank == 0 && threadIdx.x == 0) {
+    double b = 0;
+    for (int r = 0; r < ctas; ++r) b += ld_cluster_double(&total, r);
+    *p.loss = (float)b;
+  }
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its sum is being read
 }
 
 }  // namespace lmoe

@@ -84,6 +84,18 @@ cudaError_t ensure_smem_attr(K kern, int bytes, unsigned& done) {
   return e;
 }
 
+// Allows a kernel clusters of up to 16 CTAs (8 is the portable limit), once per device.
+template <typename K>
+cudaError_t allow_large_clusters(K kern, unsigned& done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const unsigned bit = 1u << (dev & 31);
+  if (done & bit) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done |= bit;
+  return e;
+}
+
 // Launches `kern` with programmatic stream serialisation, so its blocks may be scheduled while
 // the previous kernel of the stream drains (every kernel of the layer calls pdl_wait() before
 // touching data another kernel writes), and for cluster_x > 1 in clusters of cluster_x CTAs.

@@ -1,7 +1,6 @@
 // Host side of the entry points that need no layer handle and work on the caller's buffers: MXFP4
 // quantisation, dequantisation and products, and the router's balance loss.
 #include <algorithm>
-#include <cstdlib>
 #include <cstring>
 #include <type_traits>
 
@@ -105,6 +104,35 @@ Mx4Plan plan_mx4(int M, int N, int nkb, int groups, bool ragged, int sms) {
   if (nkb >= 12)
     while (split < 8 && nkb >= 8 * split && 2 * split * t128 <= (split < 4 ? sms : sms / 2)) split *= 2;
   return {128, split, (int)std::min<long long>(t128 * split, sms)};
+}
+
+// The balance loss in one launch (a cluster) or two (see balance.cuh).
+template <int NJ, int VEC, int R, int LANES>
+int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
+  constexpr int kRound = kBalThreads / LANES * R;  // rows of one round of a block
+  // One launch where a cluster streams the scores about as fast as the GPU gets through two launches
+  // more (2048 x 256: 13.5 and 12.5 us on the GPU, 16 and 19.5 us with the host's launches; 512 x 64:
+  // 6.9 and 10.5; 4096 x 256: 19 and 13)
+  const bool fits = (long long)p.S * p.E <= kBalHistInts;  // the cluster form's shared counters
+  if (fits && (long long)p.T * p.E <= (1ll << 19)) {
+    int ctas = 1;
+    while (ctas < kBalMaxCluster && ctas * kRound < p.T) ctas *= 2;  // one round of rows each
+    p.chunk = (p.T + ctas - 1) / ctas;
+    static unsigned done = 0;
+    auto kern = balance_cluster_kernel<NJ, VEC, R, LANES>;
+    CK(allow_large_clusters(kern, done));
+    CK(launch_k(kern, dim3(ctas), dim3(kBalThreads), 0, st, ctas, p));
+    return LMOE_OK;
+  }
+  CK(cudaMemsetAsync(p.counts, 0, (size_t)p.S * p.E * sizeof(int32_t), st));
+  // counting: runs of at least 64 tokens, a block an SM
+  p.chunk = std::max(64, (p.T + sms - 1) / sms);
+  CK(launch_k(balance_count_kernel, dim3((p.T + p.chunk - 1) / p.chunk), dim3(kBalThreads), 0, st, 1, p));
+  // the pass: at least one round of rows a block, at most the two blocks an SM that its registers allow
+  const int blocks = std::min(2 * sms, kBalMaxBlocks);
+  p.chunk = std::max(kRound, (p.T + blocks - 1) / blocks);
+  CK(launch_k(balance_kernel<NJ, VEC, R, LANES>, dim3((p.T + p.chunk - 1) / p.chunk), dim3(kBalThreads), 0, st, 1, p));
+  return LMOE_OK;
 }
 
 }  // namespace
@@ -292,8 +320,8 @@ int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_
   const int rc = device_sms(&sms);
   if (rc) return rc;
   cudaStream_t st = (cudaStream_t)stream;
-  CK(cudaMemsetAsync(counts, 0, (size_t)S * E * sizeof(int32_t), st));
   if (T == 0) {
+    CK(cudaMemsetAsync(counts, 0, (size_t)S * E * sizeof(int32_t), st));
     CK(cudaMemsetAsync(loss, 0, sizeof(float), st));
     return LMOE_OK;
   }
@@ -313,25 +341,19 @@ int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_
   p.done = static_cast<unsigned*>(scratch);
   p.partial = reinterpret_cast<double*>(static_cast<char*>(scratch) + 256);
   p.status = status;
-  // counting: runs of at least 256 tokens, two blocks an SM
-  p.chunk = std::max(256, (T + 2 * sms - 1) / (2 * sms));
-  CK(launch_k(balance_count_kernel, dim3((T + p.chunk - 1) / p.chunk), dim3(kBalThreads), E * sizeof(int), st, 1, p));
-  // the pass over the scores: at least a token a warp, at most eight blocks an SM
-  const int blocks = std::min(8 * sms, kBalMaxBlocks);
-  p.chunk = std::max(8, (T + blocks - 1) / blocks);
-  const dim3 grid((T + p.chunk - 1) / p.chunk), block(kBalThreads);
   const bool vec = E % 4 == 0 && (((uintptr_t)scores | (uintptr_t)dscores) & 15) == 0;
+  // sets of rows in flight: what fits 64 registers
   if (vec) {
-    if (E <= 128) CK(launch_k(balance_kernel<1, 4>, grid, block, 0, st, 1, p));
-    else if (E <= 256) CK(launch_k(balance_kernel<2, 4>, grid, block, 0, st, 1, p));
-    else if (E <= 512) CK(launch_k(balance_kernel<4, 4>, grid, block, 0, st, 1, p));
-    else CK(launch_k(balance_kernel<8, 4>, grid, block, 0, st, 1, p));
-  } else {
-    if (E <= 64) CK(launch_k(balance_kernel<2, 1>, grid, block, 0, st, 1, p));
-    else if (E <= 256) CK(launch_k(balance_kernel<8, 1>, grid, block, 0, st, 1, p));
-    else CK(launch_k(balance_kernel<32, 1>, grid, block, 0, st, 1, p));
+    if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st);
+    if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st);
+    if (E <= 128) return launch_balance<1, 4, 4, 32>(p, sms, st);
+    if (E <= 256) return launch_balance<2, 4, 4, 32>(p, sms, st);
+    if (E <= 512) return launch_balance<4, 4, 2, 32>(p, sms, st);
+    return launch_balance<8, 4, 2, 32>(p, sms, st);
   }
-  return LMOE_OK;
+  if (E <= 64) return launch_balance<2, 1, 4, 32>(p, sms, st);
+  if (E <= 256) return launch_balance<8, 1, 4, 32>(p, sms, st);
+  return launch_balance<32, 1, 1, 32>(p, sms, st);
 }
 
 }  // extern "C"
