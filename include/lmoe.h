@@ -71,6 +71,11 @@ extern "C" {
  * the expert outputs are bf16.  Needs dtype BF16 and l and h multiples of 128. */
 #define LMOE_EXPERTS_BF16 0
 #define LMOE_EXPERTS_MXFP8 1
+/* MXFP4: 4-bit operands on tcgen05.mma.kind::mxf4 (the format of the lmoe_mx4_* calls below): the
+ * expert weights quantised once at lmoe_create, the routed rows of h (bf16) and the SwiGLU
+ * activations (rounded to bf16) in every forward; products accumulate in fp32, the expert outputs are
+ * bf16.  Needs dtype BF16. */
+#define LMOE_EXPERTS_MXFP4 4
 
 /* lmoe_forward flags */
 #define LMOE_RECORD_STATS 1u    /* add this forward's scores to the QB histogram and its expert
@@ -108,7 +113,7 @@ typedef struct {
   int32_t nbins;      /* QB histogram bins; must be LMOE_NBINS */
   float rms_eps;      /* RMSNorm epsilon (1e-6) */
   int32_t max_tokens; /* largest T any forward will pass; sizes the workspace */
-  int32_t experts;    /* LMOE_EXPERTS_BF16 or LMOE_EXPERTS_MXFP8 (routed-expert operand format) */
+  int32_t experts;    /* LMOE_EXPERTS_BF16, _MXFP8 or _MXFP4 (routed-expert operand format) */
 } lmoe_config;
 
 /* Weights, all device pointers, row-major (out, in).  "dtype" means lmoe_config.dtype.
@@ -363,9 +368,13 @@ int lmoe_forward_backward(lmoe_handle *h, const lmoe_weights *w, const void *x, 
 int lmoe_mx4_bytes(int64_t rows, int32_t cols, int32_t groups, int32_t ragged, size_t *elem_bytes,
                    size_t *scale_bytes);
 
-/* Quantises x [rows, cols] (dtype LMOE_F32 or LMOE_BF16, `ld` elements from row to row). */
-int lmoe_mx4_quant(const void *x, int32_t dtype, int64_t ld, int64_t rows, int32_t cols, int32_t groups,
-                   const int32_t *offsets, uint8_t *elems, uint8_t *scales, uint32_t *status_dev, void *stream);
+/* Quantises x [rows, cols] (dtype LMOE_F32 or LMOE_BF16, `ld` elements from row to row), or, with
+ * index [rows] int32 (device), the matrix whose row r is row index[r] of x [x_rows, cols]: the rows of
+ * the tokens in the order of the routing's perm, for one.  An index outside [0, x_rows) gives a row
+ * of zeros and LMOE_STATUS_BAD_INDEX.  x_rows is not looked at without index. */
+int lmoe_mx4_quant(const void *x, int32_t dtype, int64_t ld, const int32_t *index, int64_t x_rows, int64_t rows,
+                   int32_t cols, int32_t groups, const int32_t *offsets, uint8_t *elems, uint8_t *scales,
+                   uint32_t *status_dev, void *stream);
 
 /* Quantises a SwiGLU's gate and linear projections w1, w3 [groups, h, cols] (h a multiple of 64)
  * into one matrix of 2h rows a group, interleaved as lmoe_mx4_gemm's SwiGLU form reads it: row

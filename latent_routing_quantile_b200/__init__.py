@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblmoe.so")
 
 F32, BF16 = 0, 1
-EXPERTS_BF16, EXPERTS_MXFP8 = 0, 1
+EXPERTS_BF16, EXPERTS_MXFP8, EXPERTS_MXFP4 = 0, 1, 4
 RECORD_STATS = 1
 UPDATE_BIAS = 4
 ASYNC_OUTPUT = 8
@@ -98,7 +98,7 @@ def lib() -> ctypes.CDLL:
             "lmoe_route_noalloc": [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp],
             "lmoe_watchdog_selftest": [vp, i32, vp],
             "lmoe_mx4_bytes": [i64, i32, i32, i32, POINTER(c_size_t), POINTER(c_size_t)],
-            "lmoe_mx4_quant": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp, vp],
+            "lmoe_mx4_quant": [vp, i32, i64, vp, i64, i64, i32, i32, vp, vp, vp, vp, vp],
             "lmoe_mx4_quant_w13": [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp],
             "lmoe_mx4_dequant": [vp, vp, i64, i32, i32, vp, vp, i32, i64, u32, vp, vp],
             "lmoe_mx4_gemm": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i64, u32, vp, vp],
@@ -584,12 +584,14 @@ class Mx4:
         self.offsets = offsets
 
 
-def mx4_quant(x, offsets=None, out=None, stream=None) -> Mx4:
+def mx4_quant(x, offsets=None, index=None, out=None, stream=None) -> Mx4:
     """x in MXFP4: [rows, cols] (fp32 or bf16, cols a multiple of 32, any row stride), or stacked
-    matrices [groups, rows, cols].  offsets (int32 [groups + 1]): the rows' groups, for the grouped
-    product.  out: an Mx4 of an earlier call with the same shapes, to write into."""
+    matrices [groups, rows, cols].  index (int32 [n]): the n rows x[index] instead, as routing's perm
+    names them.  offsets (int32 [groups + 1]): the rows' groups, for the grouped product.  out: an
+    Mx4 of an earlier call with the same shapes, to write into."""
     dt = _dtype(x.dtype, "x")
     shape = x.shape
+    x_rows = 0
     if len(shape) == 2:
         rows, cols = shape
         groups, stacked = 1, False
@@ -598,9 +600,13 @@ def mx4_quant(x, offsets=None, out=None, stream=None) -> Mx4:
             ld = cols
         if (step != 1 and rows and cols > 1) or ld < cols:
             raise LmoeError("x's columns must be contiguous and its rows must not overlap")
+        if index is not None:
+            if index.dtype != torch.int32 or index.dim() != 1 or not index.is_contiguous():
+                raise LmoeError("index must be a contiguous int32 tensor of one dimension")
+            x_rows, rows = rows, index.numel()
         if offsets is not None:
             groups = _offsets(offsets).numel() - 1
-    elif len(shape) == 3 and offsets is None:
+    elif len(shape) == 3 and offsets is None and index is None:
         if not x.is_contiguous():
             raise LmoeError("stacked matrices must be contiguous")
         groups, stacked = shape[0], True
@@ -608,18 +614,19 @@ def mx4_quant(x, offsets=None, out=None, stream=None) -> Mx4:
             raise LmoeError("x must hold at least one matrix")
         rows, cols, ld = groups * shape[1], shape[2], shape[2]
     else:
-        raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets")
-    dev = _device_of(x, offsets, None if out is None else out.buf)
+        raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets and index")
+    dev = _device_of(x, offsets, index, None if out is None else out.buf)
     if stream is not None or dev != _current_device():
-        with _Elsewhere(dev, stream, x, offsets, None if out is None else out.buf):
-            return mx4_quant(x, offsets, out)
+        with _Elsewhere(dev, stream, x, offsets, index, None if out is None else out.buf):
+            return mx4_quant(x, offsets, index, out)
     if out is None:
         out = Mx4(rows, cols, groups, offsets, stacked, x)
     else:
         out._match(rows, cols, groups, offsets, stacked, False)
     elems, scales = out._ptrs()
-    rc = lib().lmoe_mx4_quant(x.data_ptr(), dt, ld, rows, cols, groups, None if offsets is None else offsets.data_ptr(),
-                              elems, scales, _status_word(dev), _raw_stream(dev))
+    rc = lib().lmoe_mx4_quant(x.data_ptr(), dt, ld, None if index is None else index.data_ptr(), x_rows, rows, cols,
+                              groups, None if offsets is None else offsets.data_ptr(), elems, scales,
+                              _status_word(dev), _raw_stream(dev))
     if rc:
         _check(rc, "lmoe_mx4_quant")
     return out

@@ -305,6 +305,9 @@ struct lmoe_handle {
   uint8_t *w13q = nullptr, *w13sf = nullptr, *w2q = nullptr, *w2sf = nullptr;
   uint8_t *hq = nullptr, *hsf = nullptr, *aq = nullptr, *aqsf = nullptr, *actq = nullptr, *actsf = nullptr;
   CUtensorMap tm_aq, tm_aq_part[3], tm_w13q, tm_actq, tm_actq_part[3], tm_w2q;
+  // MXFP4 routed experts: codes and scales in the same buffers (weights, gathered rows, activations),
+  // rows in the routing's own order (not padded), and the bf16 activations in act
+  bool q4 = false;
   void *a_perm = nullptr, *act = nullptr, *o = nullptr, *z = nullptr, *a_s = nullptr;
   void *x_stage = nullptr, *y_stage = nullptr;
   // lmoe_forward_host: two input staging buffers, so the next call's host-to-device copy (on its
@@ -394,7 +397,15 @@ void plan_layout(lmoe_handle* h, Arena& a) {
   a.add((void**)&h->c, Ep * 4);
   a.add((void**)&h->wc, E * d * 8);
   if (hs) a.add(&h->ws13, h->bf ? 2 * hs * d * es : 2 * hs * 3 * d * 2);
-  if (h->q8) {
+  if (h->q4) {
+    size_t e13 = 0, s13 = 0, e2 = 0, s2 = 0;
+    lmoe_mx4_bytes(2 * (int64_t)E * hh, c.l, c.E, 0, &e13, &s13);
+    lmoe_mx4_bytes((int64_t)E * l, c.h, c.E, 0, &e2, &s2);
+    a.add((void**)&h->w13q, e13);
+    a.add((void**)&h->w13sf, s13);
+    a.add((void**)&h->w2q, e2);
+    a.add((void**)&h->w2sf, s2);
+  } else if (h->q8) {
     a.add((void**)&h->w13q, 2 * E * hh * l);
     a.add((void**)&h->w13sf, 2 * E * hh * l / 32);
     a.add((void**)&h->w2q, E * l * hh);
@@ -428,7 +439,16 @@ void plan_layout(lmoe_handle* h, Arena& a) {
   a.add((void**)&h->prow, TK * 4);
   a.add((void**)&h->pad_delta, E * 4);
   const size_t RP = (size_t)h->rows_pad;
-  if (h->q8) {
+  if (h->q4) {
+    size_t ea = 0, sa = 0, ec = 0, sc = 0;
+    lmoe_mx4_bytes((int64_t)TK, c.l, c.E, 1, &ea, &sa);
+    lmoe_mx4_bytes((int64_t)TK, c.h, c.E, 1, &ec, &sc);
+    a.add((void**)&h->aq, ea);
+    a.add((void**)&h->aqsf, sa);
+    a.add((void**)&h->actq, ec);
+    a.add((void**)&h->actsf, sc);
+    a.add(&h->act, TK * hh * es);
+  } else if (h->q8) {
     a.add((void**)&h->hq, Tm * l);
     a.add((void**)&h->hsf, Tm * l / 32);
     a.add((void**)&h->aq, RP * l);
@@ -468,7 +488,16 @@ int validate(const lmoe_config* c) {
   if (c->dtype == LMOE_BF16 && c->E % 64) return LMOE_EUNSUPPORTED;
   if (c->dtype == LMOE_F32 && c->E % 32) return LMOE_EUNSUPPORTED;
   if ((long long)c->max_tokens * c->k > (1LL << 30)) return LMOE_EUNSUPPORTED;
-  if (c->experts != LMOE_EXPERTS_BF16 && c->experts != LMOE_EXPERTS_MXFP8) return LMOE_EINVAL;
+  if (c->experts != LMOE_EXPERTS_BF16 && c->experts != LMOE_EXPERTS_MXFP8 && c->experts != LMOE_EXPERTS_MXFP4)
+    return LMOE_EINVAL;
+  if (c->experts == LMOE_EXPERTS_MXFP4) {
+    if (c->dtype != LMOE_BF16) return LMOE_EUNSUPPORTED;
+    // the 4-bit calls' own limits on the weights and on the routed rows
+    size_t e = 0, s = 0;
+    if (lmoe_mx4_bytes(2ll * c->E * c->h, c->l, c->E, 0, &e, &s) || lmoe_mx4_bytes((int64_t)c->E * c->l, c->h, c->E, 0, &e, &s) ||
+        lmoe_mx4_bytes((int64_t)c->max_tokens * c->k, std::max(c->l, c->h), c->E, 1, &e, &s))
+      return LMOE_EUNSUPPORTED;
+  }
   if (c->experts == LMOE_EXPERTS_MXFP8 && (c->dtype != LMOE_BF16 || c->l % 128 || c->h % 128))
     return LMOE_EUNSUPPORTED;
   return LMOE_OK;
@@ -502,7 +531,9 @@ int build_maps(lmoe_handle* h) {
   if (hs) ok &= make_weight_maps(h->tm_ws13, h->ws13, 2 * hs, d);
   const long long RP = h->rows_pad;
   (void)TK;
-  if (h->q8) {
+  if (h->q4) {
+    // the 4-bit calls make their own maps
+  } else if (h->q8) {
     ok &= make_map_u8(&h->tm_aq, h->aq, RP, l, l, 128);
     ok &= make_map_u8(&h->tm_actq, h->actq, RP, hh, hh, 128);
     for (int i = 0; i < 3; ++i) {
@@ -712,6 +743,12 @@ int route_from_scores(lmoe_handle* h, int T, uint32_t flags, const StatsState& p
                   (const uint8_t*)h->hsf, c.l, (const int*)h->prow, pairs, c.k, h->aq, h->aqsf));
       h->launches += 2;
     }
+    if (h->q4 && x) {  // MXFP4 experts: the pairs' rows of h (its hi part: h in bf16), quantised as they are gathered
+      int rc = lmoe_mx4_quant(h->hx, LMOE_BF16, 3ll * c.l, h->perm, T, pairs, c.l, c.E, h->offsets, h->aq, h->aqsf,
+                              h->status, st);
+      if (rc) return rc;
+      h->launches += 1;
+    }
   } else {
     // fp32 layer: all three parts of h travel with each row (the experts' split-precision products)
     CK(launch_k(gather_kernel<bf16>, ggrid, dim3(256), 0, st, 1, (const bf16*)h->hx, 3 * c.l, 3 * c.l,
@@ -857,7 +894,21 @@ int forward_bf16(lmoe_handle* h, const void* x, void* y, int T, uint32_t flags, 
   }
   // routed experts, grouped over the permuted rows
   mark(h, ST_EXPERT1, st);
-  if (h->q8) {
+  if (h->q4) {
+    // act (bf16) = silu(A W1_e^T) * (A W3_e^T), then MXFP4; o (bf16) = act W2_e^T
+    const int rows = T * c.k;
+    int rc = lmoe_mx4_gemm(h->aq, h->aqsf, h->w13q, h->w13sf, rows, 2 * c.h, c.l, c.E, h->offsets, h->act, LMOE_BF16,
+                           c.h, LMOE_MX4_SWIGLU, h->status, st);
+    if (!rc)
+      rc = lmoe_mx4_quant(h->act, LMOE_BF16, c.h, nullptr, 0, rows, c.h, c.E, h->offsets, h->actq, h->actsf, h->status,
+                          st);
+    if (rc) return rc;
+    mark(h, ST_EXPERT2, st);
+    rc = lmoe_mx4_gemm(h->actq, h->actsf, h->w2q, h->w2sf, rows, c.l, c.h, c.E, h->offsets, h->o, LMOE_BF16, c.l, 0,
+                       h->status, st);
+    if (rc) return rc;
+    h->launches += 1;  // one more than the two products of the other formats
+  } else if (h->q8) {
     static unsigned done1 = 0, done2 = 0;
     CK(ensure_smem_attr(q8_gemm_kernel<Q8_SWIGLU>, kQ8SmemBytes, done1));
     CK(ensure_smem_attr(q8_gemm_kernel<Q8_BF16>, kQ8SmemBytes, done2));
@@ -946,7 +997,7 @@ int forward_bf16(lmoe_handle* h, const void* x, void* y, int T, uint32_t flags, 
     CK(launch_tc(p, EPI_BF16, h->bn_e2, h->sms, st));
   }
   mark(h, ST_COMBINE, st);
-  CK(launch_combine((const bf16*)h->o, h->gates, h->prow, T, c.k, c.l, (bf16*)h->z, st));
+  CK(launch_combine((const bf16*)h->o, h->gates, h->q4 ? h->inv : h->prow, T, c.k, c.l, (bf16*)h->z, st));
   // y = [z | a_s] [W_up | Ws2]^T
   mark(h, ST_UP, st);
   {
@@ -1132,7 +1183,12 @@ int repack(lmoe_handle* h, const lmoe_weights* w, cudaStream_t st) {
     if (hs)
       interleave_kernel<bf16><<<grid_1d(hs * d, TPB), TPB, 0, st>>>((const bf16*)w->ws1, (const bf16*)w->ws3, g, 1,
                                                                     hs, d, (bf16*)h->ws13);
-    if (h->q8) {
+    if (h->q4) {
+      int rc = lmoe_mx4_quant_w13(w->w1, w->w3, LMOE_BF16, c.E, c.h, c.l, h->w13q, h->w13sf, h->status, st);
+      if (!rc)
+        rc = lmoe_mx4_quant(w->w2, LMOE_BF16, c.h, nullptr, 0, E * l, c.h, c.E, nullptr, h->w2q, h->w2sf, h->status, st);
+      if (rc) return rc;
+    } else if (h->q8) {
       mx_quant_w13_kernel<<<grid_1d(2 * E * hh * l / 32, TPB), TPB, 0, st>>>(
           (const bf16*)w->w1, (const bf16*)w->w3, (int)E, (int)hh, (int)l, h->w13q, h->w13sf);
       mx_quant_rows_kernel<<<grid_1d(E * l * hh / 32, TPB), TPB, 0, st>>>((const bf16*)w->w2, 1, E * l, (int)hh,
@@ -1140,7 +1196,7 @@ int repack(lmoe_handle* h, const lmoe_weights* w, cudaStream_t st) {
     } else
       interleave_kernel<bf16><<<grid_1d(E * hh * l, TPB), TPB, 0, st>>>((const bf16*)w->w1, (const bf16*)w->w3,
                                                                         nullptr, E, hh, l, (bf16*)h->w13);
-    if (!h->q8) CK(cudaMemcpyAsync(h->w2, w->w2, E * l * hh * 2, cudaMemcpyDeviceToDevice, st));
+    if (!h->q8 && !h->q4) CK(cudaMemcpyAsync(h->w2, w->w2, E * l * hh * 2, cudaMemcpyDeviceToDevice, st));
     fold_gain_kernel<bf16><<<grid_1d(d * l, TPB), TPB, 0, st>>>((const bf16*)w->w_up, nullptr, d, l,
                                                                 (bf16*)h->wy, l + hs, 0);
     if (hs)
@@ -1650,6 +1706,7 @@ static void size_handle(lmoe_handle* h, const lmoe_config* cfg) {
   h->ld_bins = (cfg->max_tokens + 31) / 32 * 32;
   h->rows_pad = (long long)cfg->max_tokens * cfg->k + (long long)kTileRows * cfg->E;
   h->q8 = cfg->experts == LMOE_EXPERTS_MXFP8;
+  h->q4 = cfg->experts == LMOE_EXPERTS_MXFP4;
   h->E_pad = h->bf ? cfg->E : (cfg->E + 63) / 64 * 64;
 }
 
@@ -1810,7 +1867,7 @@ static int forward_impl(lmoe_handle* h, const void* x, void* y, int32_t T, uint3
 int lmoe_forward_backward(lmoe_handle* h, const lmoe_weights* w, const void* x, const void* dy, void* y, int32_t T,
                           uint32_t flags, const lmoe_grads* g, void* stream) {
   if (!h || !w || !g || T < 0 || T > h->cfg.max_tokens) return LMOE_EINVAL;
-  if (!h->bf || h->q8) return LMOE_EUNSUPPORTED;
+  if (!h->bf || h->q8 || h->q4) return LMOE_EUNSUPPORTED;
   if (flags & (LMOE_UPDATE_BIAS | LMOE_ASYNC_OUTPUT)) return LMOE_EINVAL;
   const lmoe_config& c = h->cfg;
   // 128-row tiles of the weight gradients never straddle two experts or the W1 / W3 (Ws1 / Ws3)

@@ -254,8 +254,10 @@ __device__ __forceinline__ uint2 mx4_codes(const Mx4Raw<float>& r, uint32_t e) {
 }
 
 struct Mx4QuantParams {
-  const void* src;   // [rows, ld]; PAIRED: w1 [groups, h, cols]
+  const void* src;   // [rows, ld]; PAIRED: w1 [groups, h, cols]; INDEXED: [src_rows, ld]
   const void* src3;  // PAIRED: w3
+  const int* index;  // INDEXED: src's row of each row of the matrix
+  int src_rows;      // INDEXED: rows of src
   long long ld;
   int cols;
   Mx4Rows rows;
@@ -279,9 +281,11 @@ __device__ __forceinline__ constexpr int mx4_row(int n) { return (n >> 2) + 32 *
 // Bound by memory: 16384 x 7168 bf16 takes 45 us, 6.5 TB/s of values read and codes written.  With 8
 // values a lane the instructions bound it (60 us): 16 halve the maxima's exchanges and the scales'
 // arithmetic for each value.
-// PAIRED: rows are the gate and linear projections of a SwiGLU interleaved in groups of 64 (row
-// 128 (j / 64) + j % 64 = w1[j], 64 further w3[j]).
-template <typename T, bool PAIRED>
+// MX4_PAIRED: rows are the gate and linear projections of a SwiGLU interleaved in groups of 64 (row
+// 128 (j / 64) + j % 64 = w1[j], 64 further w3[j]).  MX4_INDEXED: row r is src's row index[r]; an index
+// outside src is reported and gives a row of zeros.
+enum Mx4Source : int { MX4_PLAIN = 0, MX4_PAIRED = 1, MX4_INDEXED = 2 };
+template <typename T, int SOURCE>
 __global__ void __launch_bounds__(256, 4) mx4_quant_kernel(const Mx4QuantParams p) {
   __shared__ int table[kMx4TableInts];
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // rows in flight a half-warp
@@ -292,6 +296,7 @@ __global__ void __launch_bounds__(256, 4) mx4_quant_kernel(const Mx4QuantParams 
   const unsigned nkb = (unsigned)mx4_kblocks(p.cols);
   const unsigned n = (unsigned)tiles.total * nkb * 8;  // less than 2^31, as the host has seen to
   const long long pitch = p.cols >> 1;
+  constexpr bool PAIRED = SOURCE == MX4_PAIRED, INDEXED = SOURCE == MX4_INDEXED;
   const long long to3 = PAIRED ? static_cast<const T*>(p.src3) - static_cast<const T*>(p.src) : 0;
   for (unsigned u = blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += gridDim.x * 8) {
     const int sl = (int)(u & 7);
@@ -307,8 +312,19 @@ __global__ void __launch_bounds__(256, 4) mx4_quant_kernel(const Mx4QuantParams 
       // n % 4 = 2, 3
       const int within = row0 - g * tiles.group_rows;
       src = static_cast<const T*>(p.src) + ((long long)g * (tiles.group_rows >> 1) + (within >> 1) + 4 * sl) * p.ld + c;
+    } else if constexpr (INDEXED) {
+      src = static_cast<const T*>(p.src) + c;
     } else {
       src = static_cast<const T*>(p.src) + (long long)(row0 + 4 * sl) * p.ld + c;
+    }
+    int from = 0;  // INDEXED: lane n holds src's row of row n, -1 for none
+    if constexpr (INDEXED) {
+      const int r = 4 * sl + mx4_row(lane & 15);
+      if (r < valid) from = p.index[row0 + r];
+      if ((unsigned)from >= (unsigned)p.src_rows) {
+        from = -1;
+        set_status(p.status, LMOE_STATUS_BAD_INDEX);
+      }
     }
     uint8_t* dst = p.elems + (long long)(row0 + 4 * sl) * pitch + (c >> 1);
     // rows from the slice's first on that exist (cols is a multiple of 32: a block is inside or outside)
@@ -321,8 +337,14 @@ __global__ void __launch_bounds__(256, 4) mx4_quant_kernel(const Mx4QuantParams 
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int r = mx4_row(2 * (b + i)) + 32 * half;  // row 2 (b + i) + half of the slice
-          const long long at = PAIRED ? (long long)(r & 63) * p.ld + ((r & 64) ? to3 : 0) : (long long)r * p.ld;
-          if (decltype(whole)::value || r < left) {
+          long long at = PAIRED ? (long long)(r & 63) * p.ld + ((r & 64) ? to3 : 0) : (long long)r * p.ld;
+          bool some = decltype(whole)::value || r < left;
+          if constexpr (INDEXED) {
+            const int f = __shfl_sync(0xffffffffu, from, 2 * (b + i) + half);
+            at = (long long)f * p.ld;
+            some = some && f >= 0;
+          }
+          if (some) {
             mx4_load16(src + at, p.access, raw[i]);
           } else {
 #pragma unroll

@@ -149,21 +149,25 @@ int lmoe_mx4_bytes(int64_t rows, int32_t cols, int32_t groups, int32_t ragged, s
   return LMOE_OK;
 }
 
-int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t cols, int32_t groups,
-                   const int32_t* offsets, uint8_t* elems, uint8_t* scales, uint32_t* status, void* stream) {
+int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, const int32_t* index, int64_t x_rows, int64_t rows,
+                   int32_t cols, int32_t groups, const int32_t* offsets, uint8_t* elems, uint8_t* scales,
+                   uint32_t* status, void* stream) {
   const int rc = check_rows(rows, cols, groups, offsets != nullptr);
   if (rc) return rc;
   if (dtype != LMOE_F32 && dtype != LMOE_BF16) return LMOE_EINVAL;
+  if (index && (x_rows < 0 || x_rows > INT32_MAX)) return LMOE_EINVAL;
   if (rows == 0) return LMOE_OK;
   if (!x || !elems || !scales || !status || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
     return LMOE_EINVAL;
-  if ((uintptr_t)x % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
+  if ((uintptr_t)x % (dtype == LMOE_F32 ? 4 : 2) || (uintptr_t)index % 4) return LMOE_EINVAL;
   int sms = 0;
   const int drc = device_sms(&sms);
   if (drc) return drc;
   Mx4QuantParams p;
   memset(&p, 0, sizeof(p));
   p.src = x;
+  p.index = index;
+  p.src_rows = (int)x_rows;
   p.ld = ld;
   p.cols = cols;
   p.rows = Mx4Rows{offsets, groups, (int)rows};
@@ -173,10 +177,14 @@ int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32
   p.access = row_access(x, ld, dtype);
   const int grid = mx4_grid(work_tiles(rows, groups, offsets != nullptr), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == LMOE_F32)
-    CK(launch_k(mx4_quant_kernel<float, false>, dim3(grid), dim3(256), 0, st, 1, p));
-  else
-    CK(launch_k(mx4_quant_kernel<bf16, false>, dim3(grid), dim3(256), 0, st, 1, p));
+  const dim3 g(grid), b(256);
+  if (index) {
+    if (dtype == LMOE_F32) CK(launch_k(mx4_quant_kernel<float, MX4_INDEXED>, g, b, 0, st, 1, p));
+    else CK(launch_k(mx4_quant_kernel<bf16, MX4_INDEXED>, g, b, 0, st, 1, p));
+  } else {
+    if (dtype == LMOE_F32) CK(launch_k(mx4_quant_kernel<float, MX4_PLAIN>, g, b, 0, st, 1, p));
+    else CK(launch_k(mx4_quant_kernel<bf16, MX4_PLAIN>, g, b, 0, st, 1, p));
+  }
   return LMOE_OK;
 }
 
@@ -208,9 +216,9 @@ int lmoe_mx4_quant_w13(const void* w1, const void* w3, int32_t dtype, int32_t gr
   const int grid = mx4_grid(work_tiles(rows, groups, false), mx4_kblocks(cols), sms);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == LMOE_F32)
-    CK(launch_k(mx4_quant_kernel<float, true>, dim3(grid), dim3(256), 0, st, 1, p));
+    CK(launch_k(mx4_quant_kernel<float, MX4_PAIRED>, dim3(grid), dim3(256), 0, st, 1, p));
   else
-    CK(launch_k(mx4_quant_kernel<bf16, true>, dim3(grid), dim3(256), 0, st, 1, p));
+    CK(launch_k(mx4_quant_kernel<bf16, MX4_PAIRED>, dim3(grid), dim3(256), 0, st, 1, p));
   return LMOE_OK;
 }
 

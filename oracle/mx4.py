@@ -79,3 +79,28 @@ def swiglu_columns(c):
 def silu(x):
     with np.errstate(over="ignore"):
         return x / (1.0 + np.exp(-x))
+
+
+def bf16(a) -> np.ndarray:
+    """Nearest bf16 values (torch's cast)."""
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16).double().numpy()
+
+
+def layer_forward_mxfp4(x, w: dict, b, k: int, eps: float = 1e-6) -> np.ndarray:
+    """The layer with MXFP4 routed experts: the forward oracle's steps, the experts' products on the MXFP4
+    values of bf16 rows of h, of the weights, and of the activations rounded to bf16."""
+    import oracle
+    r = oracle.layer_routing(x, w, b, k, eps)
+    h, idx = bf16(r["h"]), r["idx"]
+    o = np.zeros(idx.shape + (h.shape[1],))
+    for e in np.unique(idx):
+        t, i = np.nonzero(idx == e)
+        w1, w3, w2 = (values(oracle.f64(w[n][e])) for n in ("w1", "w3", "w2"))
+        a = values(h[t])
+        o[t, i] = values(bf16(silu(a @ w1.T) * (a @ w3.T))) @ w2.T
+    y = oracle.up_projection(oracle.combine(r["gates"], o), oracle.f64(w["w_up"]))
+    if "ws1" in w:
+        x_hat = oracle.rmsnorm(oracle.f64(x), oracle.f64(w["rms_gain"]), eps)
+        y = y + oracle.shared_expert(x_hat, oracle.f64(w["ws1"]), oracle.f64(w["ws3"]), oracle.f64(w["ws2"]))
+    return y

@@ -12,7 +12,9 @@ import numpy as np
 import pytest
 import torch
 
+import datagen
 import latent_routing_quantile_b200 as lq
+import oracle
 import oracle.mx4 as mx
 
 pytestmark = pytest.mark.gpu
@@ -128,6 +130,25 @@ def test_ragged_groups_and_rows_of_none(head, sizes, tail):
     assert np.array_equal(k[inside], ref[inside]) and (k[:head] == 7).all() and (k[M - tail:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_indexed_rows(dtype, grouped):
+    x = rows((50, 352), 19, dtype)
+    g = torch.Generator().manual_seed(2)
+    idx = torch.randint(0, 50, (300,), generator=g).int()
+    idx[7] = idx[8] = idx[250] = 3  # the same row again
+    off = ragged(300, [10, 0, 150, 140]) if grouped else None
+    q = lq.mx4_quant(x.cuda(), offsets=None if off is None else off.cuda(), index=idx.cuda())
+    ref = mx.values(np64(x))[idx.numpy()]
+    assert np.array_equal(np64(lq.mx4_dequant(q, dtype=torch.float32)), ref)
+    bad = idx.clone()
+    bad[4], bad[299] = 50, -1
+    q = lq.mx4_quant(x.cuda(), offsets=None if off is None else off.cuda(), index=bad.cuda(), out=q)
+    assert lq.op_status() == lq.STATUS_BAD_INDEX
+    ref[4] = ref[299] = 0
+    assert np.array_equal(np64(lq.mx4_dequant(q, dtype=torch.float32)), ref)
+
+
 def test_many_groups_and_more_tiles_than_blocks():
     rng = np.random.default_rng(3)
     sizes = rng.integers(0, 40, 1024)
@@ -156,7 +177,11 @@ def check_product(got, c, mag, K, out):
 
 
 SIZES = [(1, 1, 32), (1, 7, 64), (1, 1000, 512), (7, 129, 96), (128, 128, 256), (129, 257, 288), (333, 1000, 992),
-         (1025, 384, 544), (64, 2048, 2048), (513, 640, 1280)]
+         (1025, 384, 544), (64, 2048, 2048), (513, 640, 1280),
+         # K split over clusters of 2, 4 and 8 CTAs, their shares uneven
+         (130, 4100, 3104), (70, 1000, 4128), (1, 130, 7200), (33, 250, 16416),
+         # 256-wide tiles: a last one half outside, columns off the 16-byte grid, several tiles a CTA
+         (2100, 2050, 96), (3001, 1700, 544), (5000, 2190, 288)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -182,7 +207,8 @@ def test_product_into_strided_output_leaves_the_rest(out, pitch):
 
 
 GROUPS = [(0, [5, 0, 130, 1, 0, 256], 0), (3, [1, 1, 1], 9), (0, [0, 0], 4), (0, [200], 0), (2, [31, 33, 127, 128, 129], 1),
-          (0, [1] * 16, 0), (0, [300, 0, 0, 290, 310, 33, 600, 2], 0)]
+          (0, [1] * 16, 0), (0, [300, 0, 0, 290, 310, 33, 600, 2], 0),
+          (5, list(range(0, 270, 3)), 6)]  # 90 groups: 256-wide tiles at N >= 257
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -214,7 +240,8 @@ def check_swiglu(got, c, mag, K):
     assert (err <= tol).all(), float((err - tol).max())
 
 
-@pytest.mark.parametrize("M,h,K", [(1, 64, 32), (5, 192, 288), (129, 128, 512), (300, 512, 2048), (1030, 320, 256)])
+@pytest.mark.parametrize("M,h,K", [(1, 64, 32), (5, 192, 288), (129, 128, 512), (300, 512, 2048), (1030, 320, 256),
+                                   (70, 192, 4128), (3, 64, 7200), (3001, 1088, 288), (2300, 1984, 96)])
 def test_dense_swiglu(M, h, K):
     a, w1, w3 = rows((M, K), 3), rows((h, K), 4, spread=0) / K ** 0.5, rows((h, K), 5, spread=0)
     act = lq.mx4_gemm(lq.mx4_quant(a.cuda()), lq.mx4_quant_w13(w1.cuda(), w3.cuda()), swiglu=True)
@@ -322,13 +349,68 @@ def test_experts_after_routing():
     w1, w3, w2 = (rows(s, 82 + i, spread=0) / s[2] ** 0.5 for i, s in enumerate(((E, h, l), (E, h, l), (E, l, h))))
     w13, wd = lq.mx4_quant_w13(w1.cuda(), w3.cuda()), lq.mx4_quant(w2.cuda())
     xp = x[r["perm"].long()]
-    act = lq.mx4_gemm(lq.mx4_quant(xp, offsets=r["offsets"]), w13, swiglu=True)
+    act = lq.mx4_gemm(lq.mx4_quant(x, offsets=r["offsets"], index=r["perm"]), w13, swiglu=True)
     o = lq.mx4_gemm(lq.mx4_quant(act, offsets=r["offsets"]), wd)
     off = r["offsets"].cpu().numpy()
     b = np.stack([mx.values(np64(w1)).reshape(E, -1, 64, l), mx.values(np64(w3)).reshape(E, -1, 64, l)], 2)
     check_swiglu(np64(act), *mx.product(mx.values(np64(xp)), b.reshape(E, 2 * h, l), off), l)
     c, mag = mx.product(mx.values(np64(act)), mx.values(np64(w2)), off)
     check_product(np64(o), c, mag, h, torch.bfloat16)
+
+
+@pytest.mark.parametrize("name,T,d,l,E,k,h,hs", [
+    ("mx4_small", 1000, 256, 128, 64, 4, 128, 256),
+    ("mx4_ragged", 333, 256, 192, 64, 3, 64, 0),        # widths that fill no tile, no shared expert
+    ("mx4_one", 1, 256, 128, 64, 4, 128, 256),          # a single token
+    ("mx4_mini", 8192, 1024, 256, 256, 6, 256, 2048),   # mini_replica widths
+])
+def test_layer_with_4_bit_experts(name, T, d, l, E, k, h, hs):
+    """Layer(experts=EXPERTS_MXFP4): routing identical to the oracle's; outputs within 1e-2 normwise of the
+    float64 layer with MXFP4 experts (the bf16 roundings of o, z, a_s and y, at most 2^-8 each and
+    independent, and the rare code that a rounding of h or of an activation moves), and at least five
+    times as far from the bf16-expert oracle, so the 4-bit path is the one that ran."""
+    shape = datagen.LayerShape(name, T, d, l, E, k, h, hs, "bf16", seed=83, offset_var=0.5)
+    w, x = datagen.layer_weights(shape), datagen.tokens(shape)
+    layer = lq.layer_from_weights(shape, w, experts=lq.EXPERTS_MXFP4)
+    y = layer.forward(x.cuda(), record_stats=True)
+    again = layer.forward(x.cuda(), y=torch.empty_like(y))
+    r = layer.routing()
+    torch.cuda.synchronize()
+    assert torch.equal(y, again)
+    pick = np.arange(T) if T <= 1000 else np.arange(0, T, 16)
+    xs = x[torch.from_numpy(pick)]
+    ro = oracle.layer_routing(xs, w, np.zeros(E), k, shape.rms_eps)
+    assert np.array_equal(r["idx"].cpu().numpy()[pick], ro["idx"])
+    yg = y.float().cpu().numpy()[pick]
+    y4 = mx.layer_forward_mxfp4(xs, w, np.zeros(E), k, shape.rms_eps)
+    y16 = oracle.layer_forward(xs, w, np.zeros(E), k, shape.rms_eps)["y"]
+    norm = lambda a, b: float(np.linalg.norm(a - b) / np.linalg.norm(b))
+    err4, err16 = norm(yg, y4), norm(yg, y16)
+    print(name, err4, err16)
+    assert err4 <= 1e-2 and err16 >= 5 * err4, (err4, err16)
+    assert layer.status() == 0
+    with pytest.raises(lq.LmoeError, match="unsupported"):
+        layer.forward_backward(x.cuda(), x.cuda(), {n: t.cuda() for n, t in w.items()})
+    layer.close()
+
+
+def test_layer_with_4_bit_experts_replays_and_updates():
+    """Repeated forwards (replayed as a graph), another T on the same handle, and the bias update inside."""
+    shape = datagen.LayerShape("mx4_replay", 700, 256, 128, 64, 4, 128, 256, "bf16", seed=85, offset_var=0.5)
+    w, x = datagen.layer_weights(shape), datagen.tokens(shape).cuda()
+    layer = lq.layer_from_weights(shape, w, experts=lq.EXPERTS_MXFP4)
+    y, x2 = torch.empty_like(x), x.clone()
+    first = layer.forward(x2, y=y).clone()
+    for _ in range(3):
+        assert torch.equal(layer.forward(x2, y=y), first)
+    x2.copy_(x.flip(0))
+    assert torch.equal(layer.forward(x2, y=y), first.flip(0))
+    part = layer.forward(x[:130].contiguous()).float()  # other tiles, and sums in another order
+    assert (part - first[:130].float()).norm() <= 1e-2 * first[:130].float().norm()
+    layer.set_update(0.05)
+    layer.forward(x, update_bias=True)
+    assert layer.bias().abs().max() > 0 and layer.status() == 0
+    layer.close()
 
 
 def test_full_sized_products_on_sampled_rows():

@@ -112,9 +112,12 @@ P = 1 << 20  # a pointer that is aligned and never read
 @pytest.mark.parametrize("change,code", [
     (dict(cols=33), EUNSUPPORTED), (dict(rows=-1), EINVAL), (dict(groups=0), EINVAL), (dict(dtype=2), EINVAL),
     (dict(ld=63), EINVAL), (dict(x=None), EINVAL), (dict(x=P + 1), EINVAL), (dict(elems=P + 8), EINVAL),
-    (dict(scales=None), EINVAL), (dict(status=None), EINVAL), (dict(groups=2, rows=5), EINVAL), (dict(rows=0), 0)])
+    (dict(scales=None), EINVAL), (dict(status=None), EINVAL), (dict(groups=2, rows=5), EINVAL), (dict(rows=0), 0),
+    (dict(index=P + 2), EINVAL), (dict(index=P, x_rows=-1), EINVAL), (dict(index=P, x_rows=1 << 31), EINVAL),
+    (dict(rows=1 << 30, cols=1 << 20, ld=1 << 20), EUNSUPPORTED)])
 def test_quant_refusals(L, change, code):
-    a = dict(x=P, dtype=1, ld=64, rows=4, cols=64, groups=1, offsets=None, elems=P, scales=P, status=P, stream=None)
+    a = dict(x=P, dtype=1, ld=64, index=None, x_rows=0, rows=4, cols=64, groups=1, offsets=None, elems=P, scales=P,
+             status=P, stream=None)
     a.update(change)
     assert L.lmoe_mx4_quant(*a.values()) == code
 
@@ -178,8 +181,18 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         lq.balance_loss(torch.zeros(4), torch.zeros(4, 2, dtype=torch.int32), 0.1)
 
 
+def test_layer_with_4_bit_experts_is_sized_and_checked():
+    a = dict(d=1024, l=256, E=256, k=6, h=256, hs=2048, dtype=lq.BF16, max_tokens=8192)
+    n4, n8 = (lq.workspace_bytes(**a, experts=e) for e in (lq.EXPERTS_MXFP4, lq.EXPERTS_MXFP8))
+    assert 0 < n4 < n8
+    lq.workspace_bytes(**{**a, "l": 192, "h": 64}, experts=lq.EXPERTS_MXFP4)
+    with pytest.raises(lq.LmoeError, match="unsupported"):
+        lq.workspace_bytes(256, 64, 32, 4, 128, 512, lq.F32, 256, experts=lq.EXPERTS_MXFP4)
+
+
 def test_flag_constants_match_the_header():
     import os, re
     text = open(os.path.join(os.path.dirname(lq.__file__), "..", "include", "lmoe.h")).read()
-    for name, v in (("MX4_SWIGLU", lq.MX4_SWIGLU), ("MX4_ZERO_REST", lq.MX4_ZERO_REST)):
-        assert int(re.search(rf"#define LMOE_{name} (\d+)u", text).group(1)) == v
+    for name, v in (("MX4_SWIGLU", lq.MX4_SWIGLU), ("MX4_ZERO_REST", lq.MX4_ZERO_REST),
+                    ("EXPERTS_MXFP4", lq.EXPERTS_MXFP4)):
+        assert int(re.search(rf"#define LMOE_{name} (\d+)", text).group(1)) == v
