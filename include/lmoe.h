@@ -408,8 +408,8 @@ int lmoe_mx4_gemm(const uint8_t *a_elems, const uint8_t *a_scales, const uint8_t
  *   L = coef / S' sum_q sum_e f_qe mean_{t in q} (s_te / sum_j s_tj),   f_qe = counts[q, e] E / (k n_q)
  * for n_q tokens in q, and, when dscores [T, E] is given, its gradient dL/ds.  The choice is
  * piecewise constant: no gradient flows through the counts.  A token outside every sequence takes
- * no part and gets a zero gradient; so does a token whose scores are all zero.  A NaN score makes the
- * loss and its token's gradient NaN and sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index
+ * no part and gets a zero gradient; so does a token whose scores sum to zero.  A NaN or infinite
+ * score makes the loss and its token's gradient NaN and sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index
  * other than -1 outside [0, E) is not counted, and it, or cu_seqlens that decrease or leave [0, T],
  * sets LMOE_STATUS_BAD_INDEX (the bits are ORed in, never cleared).
  * E at most 1024, k at most 32.  scratch is lmoe_balance_scratch_bytes of device memory, 16-byte
@@ -419,6 +419,20 @@ int lmoe_balance_scratch_bytes(size_t *bytes);
 int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_t E, int32_t k,
                       const int32_t *cu_seqlens, int32_t S, float coef, int32_t *counts, float *loss, float *dscores,
                       void *scratch, uint32_t *status_dev, void *stream);
+
+/* The balance loss in the training step: every later lmoe_forward_backward adds the loss of its own
+ * scores and choice, with weight coef, to the loss it differentiates (its gradient reaches the router,
+ * and through it h and x); coef == 0 takes it out again.  cu_seqlens [S + 1] (NULL: one sequence of all
+ * the step's tokens) stays the caller's, is read by each step and must live as long; the bounds may
+ * change between steps, S by another call only.  Bounds that decrease or leave [0, T] set
+ * LMOE_STATUS_BAD_INDEX in the handle's status word, and that step has no balance loss.  Layers that
+ * lmoe_forward_backward takes only (LMOE_EUNSUPPORTED).  Allocates (about 4 max_tokens E bytes) and
+ * synchronises the device: not for a stream capture. */
+int lmoe_set_balance(lmoe_handle *h, float coef, const int32_t *cu_seqlens, int32_t S);
+
+/* The last training step's balance loss [1] and counts [S, E] (device, either may be NULL), while
+ * lmoe_set_balance has it on. */
+int lmoe_get_balance(lmoe_handle *h, float *loss, int32_t *counts, void *stream);
 
 #ifdef __cplusplus
 }

@@ -35,7 +35,7 @@ EXPORTED = (
     "lmoe_profile_enable", "lmoe_profile_read", "lmoe_stage_name", "lmoe_launch_count",
     "lmoe_route_noalloc", "lmoe_watchdog_selftest", "lmoe_gemm_bf16_ex", "lmoe_forward_backward",
     "lmoe_mx4_bytes", "lmoe_mx4_quant", "lmoe_mx4_quant_w13", "lmoe_mx4_dequant", "lmoe_mx4_gemm",
-    "lmoe_balance_scratch_bytes", "lmoe_balance_loss",
+    "lmoe_balance_scratch_bytes", "lmoe_balance_loss", "lmoe_set_balance", "lmoe_get_balance",
 )
 NUM_STAGES = 14
 
@@ -103,6 +103,8 @@ def lib() -> ctypes.CDLL:
             "lmoe_mx4_dequant": [vp, vp, i64, i32, i32, vp, vp, i32, i64, u32, vp, vp],
             "lmoe_mx4_gemm": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i64, u32, vp, vp],
             "lmoe_balance_scratch_bytes": [POINTER(c_size_t)],
+            "lmoe_set_balance": [vp, c_float, vp, i32],
+            "lmoe_get_balance": [vp, vp, vp, vp],
             "lmoe_balance_loss": [vp, vp, i32, i32, i32, vp, i32, c_float, vp, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
@@ -264,6 +266,25 @@ class Layer:
         """Step and rule of the update that forward(..., update_bias=True) runs after its routing."""
         flags = (QB_LITERAL if literal else 0) | (BIAS_SIGN if sign_rule else 0)
         _check(lib().lmoe_set_update(self.handle, float(beta), flags), "lmoe_set_update")
+
+    def set_balance(self, coef, cu_seqlens=None):
+        """The router's balance loss in every later forward_backward (weight coef; 0 takes it out), sequence
+        by sequence for bounds cu_seqlens (int32 [S + 1] on the device, read at each step; None: the
+        step's tokens are one sequence)."""
+        S = 1
+        if cu_seqlens is not None:
+            _dev(_offsets(cu_seqlens, "cu_seqlens"), name="cu_seqlens")
+            S = cu_seqlens.numel() - 1
+        _check(lib().lmoe_set_balance(self.handle, float(coef), _ptr(cu_seqlens), S), "lmoe_set_balance")
+        self._balance = (cu_seqlens, S)  # the bounds stay alive as long as the steps read them
+
+    def balance(self, stream=None):
+        """(loss [1], counts [S, E]) of the last training step with a balance loss."""
+        _, S = getattr(self, "_balance", (None, 1))
+        loss = torch.empty(1, dtype=torch.float32, device="cuda")
+        counts = torch.empty((S, self.cfg.E), dtype=torch.int32, device="cuda")
+        _check(lib().lmoe_get_balance(self.handle, _ptr(loss), _ptr(counts), _stream(stream)), "lmoe_get_balance")
+        return loss, counts
 
     # ---------------------------------------------------------------- introspection
     def routing(self, stream=None):

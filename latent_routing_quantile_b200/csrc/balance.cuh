@@ -105,7 +105,7 @@ __device__ __forceinline__ void bal_count(const BalanceParams& p, int lo, int hi
 // The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe.  LANES lanes share a row (a warp
 // takes 32 / LANES rows side by side) and R such sets of rows are in flight; lane l of a row holds experts
 // VEC (l + LANES j) .. + VEC - 1.  Returns the lane's sum of D (lane 0 of each row's); nan: some score
-// was a NaN.
+// was a NaN or infinite.
 template <int NJ, int VEC, int R, int LANES>
 __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
   constexpr int kSide = 32 / LANES;
@@ -163,7 +163,7 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
       g[r] = wq * inv;
       if (t0 + r * kSide < hi) {
         if (lane == 0) acc += dot[r];
-        nan |= sum[r] != sum[r];
+        nan |= !(fabsf(sum[r]) <= 3.4028234e38f);
       }
     }
     if (p.dscores) {

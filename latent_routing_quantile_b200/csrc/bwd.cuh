@@ -44,13 +44,16 @@ __global__ void __launch_bounds__(256) xhat_kernel(const bf16* __restrict__ x, c
 //   dL/dlogit_i = dL/ds_i s_i (1 - s_i)  (s = sigmoid of the logit).
 // dlogit [T, E] bf16 is written whole (zeros but for the k chosen experts) for the router's
 // GEMMs; dlp holds each pair's logit gradient in fp32 at its padded row, for the column offsets'
-// gradient.
+// gradient.  ds_aux (a training step with a balance loss): the gradient that all scores get besides,
+// dL/ds_aux [T, E]; its logit gradient ds_aux s (1 - s) joins dlogit and replaces ds_aux, for the
+// column offsets' gradient.
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const bf16* __restrict__ dz, const bf16* __restrict__ o,
                                                           const int* __restrict__ prow,
                                                           const float* __restrict__ gates,
                                                           const int* __restrict__ idx, const float* __restrict__ s,
                                                           int ntok, int k, int l, int E, bf16* __restrict__ d_o,
-                                                          bf16* __restrict__ dlogit, float* __restrict__ dlp) {
+                                                          bf16* __restrict__ dlogit, float* __restrict__ dlp,
+                                                          float* __restrict__ ds_aux) {
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -96,10 +99,32 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const bf16* __restrict
   const float ds = (dg_l - G) / S;
   const float dl = ds * s_l * (1.f - s_l);
   uint4* lrow = reinterpret_cast<uint4*>(dlogit + (size_t)t * E);
-  for (int v = lane; v < E / 8; v += 32) lrow[v] = make_uint4(0, 0, 0, 0);
+  float dl_aux = 0.f;
+  if (ds_aux) {
+    float4* arow = reinterpret_cast<float4*>(ds_aux + (size_t)t * E);
+    const float4* srow = reinterpret_cast<const float4*>(s + (size_t)t * E);
+    for (int v = lane; v < E / 8; v += 32) {
+      uint4 out;
+      uint32_t* ow = &out.x;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 a = arow[2 * v + q], sv = srow[2 * v + q];
+        const float4 o4 = make_float4(a.x * sv.x * (1.f - sv.x), a.y * sv.y * (1.f - sv.y), a.z * sv.z * (1.f - sv.z),
+                                      a.w * sv.w * (1.f - sv.w));
+        arow[2 * v + q] = o4;
+        ow[2 * q] = pack_bf16x2(o4.x, o4.y);
+        ow[2 * q + 1] = pack_bf16x2(o4.z, o4.w);
+      }
+      lrow[v] = out;
+    }
+    __syncwarp();
+    if (lane < k) dl_aux = ds_aux[(size_t)t * E + e_l];
+  } else {
+    for (int v = lane; v < E / 8; v += 32) lrow[v] = make_uint4(0, 0, 0, 0);
+  }
   __syncwarp();
   if (lane < k) {
-    dlogit[(size_t)t * E + e_l] = __float2bfloat16_rn(dl);
+    dlogit[(size_t)t * E + e_l] = __float2bfloat16_rn(dl + dl_aux);
     dlp[r_l] = dl;
   }
 }
@@ -143,6 +168,41 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const int* __restrict__ 
 #pragma unroll
   for (int off = 16; off; off >>= 1) acc += __shfl_xor_sync(kFull, acc, off);
   if (lane == 0) dc[e] = acc;
+}
+
+// Column sums of the balance loss's logit gradients [ntok, E]: a block sums kAuxRows rows, and
+// aux_bias_grad_kernel adds the blocks' sums, in their order, to dL/dc.
+constexpr int kAuxRows = 64;
+__global__ void __launch_bounds__(256) aux_colsum_kernel(const float* __restrict__ dl, int ntok, int E,
+                                                         float* __restrict__ part) {
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.x * kAuxRows, t1 = min(ntok, t0 + kAuxRows);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float acc = 0.f;
+#pragma unroll 8
+    for (int t = t0; t < t1; ++t) acc += dl[(size_t)t * E + e];
+    part[(size_t)blockIdx.x * E + e] = acc;
+  }
+}
+__global__ void __launch_bounds__(256) aux_bias_grad_kernel(const float* __restrict__ part, int nrows, int E,
+                                                            float* __restrict__ dc) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float sm[8][33];
+  const int e = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+  float acc = 0.f;
+  if (e < E)
+#pragma unroll 4
+    for (int i = y; i < nrows; i += 8) acc += part[(size_t)i * E + e];
+  sm[y][threadIdx.x & 31] = acc;
+  __syncthreads();
+  if (y == 0 && e < E) {
+    float s = dc[e];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += sm[j][threadIdx.x];
+    dc[e] = s;
+  }
 }
 
 // dh[t] = dh_router[t] + sum_i dh_expert[row of pair (t, i)], one warp per token; fp32 sums, the

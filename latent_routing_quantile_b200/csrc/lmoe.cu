@@ -372,6 +372,16 @@ struct lmoe_handle {
   long long g_tick = 0;
   long long g_used[2] = {0, 0};
   BwdWork* bw = nullptr;
+  // balance loss of the training steps (lmoe_set_balance): its weight, the caller's sequence bounds, and
+  // its buffers (one allocation)
+  bool bal_on = false;
+  float bal_coef = 0.f;
+  const int* bal_cu = nullptr;
+  int bal_S = 0, bal_cap = 0;  // sequences; those its buffers hold
+  void* bal_mem = nullptr;
+  float *bal_ds = nullptr, *bal_loss = nullptr, *bal_part = nullptr;
+  int* bal_counts = nullptr;
+  void* bal_scratch = nullptr;
 };
 
 namespace {
@@ -1508,10 +1518,16 @@ int backward_bf16(lmoe_handle* h, const lmoe_weights* w, const void* x, const vo
     int rc = dense_gemm(h, p, EPI_BF16, T, (int)l, st);
     if (rc) return rc;
   }
+  if (h->bal_on) {  // the balance loss of this step's scores and choice, and its gradient in the scores
+    int rc = lmoe_balance_loss(h->s, h->idx, T, c.E, c.k, h->bal_cu, h->bal_S, h->bal_coef, h->bal_counts, h->bal_loss,
+                               h->bal_ds, h->bal_scratch, h->status, st);
+    if (rc) return rc;
+    h->launches += 1;
+  }
   // combine and gates: dL/do of every pair, dL/dlogit
   CK(launch_k(combine_bwd_kernel, dim3((T + 7) / 8), dim3(256), 0, st, 1, (const bf16*)b->dz, (const bf16*)h->o,
               (const int*)h->prow, (const float*)h->gates, (const int*)h->idx, (const float*)h->s, T, c.k, (int)l,
-              (int)E, b->d_o, b->dlogit, b->dlp));
+              (int)E, b->d_o, b->dlogit, b->dlp, h->bal_on ? h->bal_ds : (float*)nullptr));
   h->launches += 1;
   {  // routed experts: dL/d act_e = dL/do W2_e, through the SwiGLU (pre-activations saved by the
      // forward): [dL/dp1 | dL/dp3] (zero past each expert's rows)
@@ -1596,6 +1612,13 @@ int backward_bf16(lmoe_handle* h, const lmoe_weights* w, const void* x, const vo
   CK(launch_k(bias_grad_kernel, dim3((unsigned)((E + 7) / 8)), dim3(256), 0, st, 1, (const int*)h->offsets,
               (const int*)h->pad_delta, (const int*)h->counts, (const float*)b->dlp, (int)E, g->router_bias));
   h->launches += 1;
+  if (h->bal_on) {
+    const int nblk = (T + kAuxRows - 1) / kAuxRows;
+    CK(launch_k(aux_colsum_kernel, dim3(nblk), dim3(256), 0, st, 1, (const float*)h->bal_ds, T, (int)E, h->bal_part));
+    CK(launch_k(aux_bias_grad_kernel, dim3((unsigned)((E + 31) / 32)), dim3(256), 0, st, 1, (const float*)h->bal_part,
+                nblk, (int)E, g->router_bias));
+    h->launches += 2;
+  }
   {
     TcParams p = tc_base(h);
     p.tmA[0] = p.tmA[1] = dlg_mn;
@@ -1790,6 +1813,7 @@ int lmoe_destroy(lmoe_handle* h) {
   if (!h) return LMOE_EINVAL;
   cudaDeviceSynchronize();
   bwd_free(h);
+  cudaFree(h->bal_mem);
   for (auto& r : h->prof)
     for (auto& e : r.ev) cudaEventDestroy(e);
   for (auto& g : h->g_fwd) g.reset(nullptr, nullptr, -1, 0, 0.f, 0);
@@ -1994,6 +2018,58 @@ int lmoe_set_update(lmoe_handle* h, float beta, uint32_t flags) {
   h->upd_beta = beta;
   h->upd_flags = flags & (LMOE_QB_LITERAL | LMOE_BIAS_SIGN);
   h->upd_set = true;
+  return LMOE_OK;
+}
+
+int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int32_t S) {
+  if (!h || !(coef == coef) || S <= 0 || (!cu_seqlens && S != 1) || (uintptr_t)cu_seqlens % 4) return LMOE_EINVAL;
+  if (!h->bf || h->q8 || h->q4) return LMOE_EUNSUPPORTED;  // as lmoe_forward_backward
+  const size_t Tm = h->cfg.max_tokens, E = h->cfg.E;
+  if (coef != 0.f && h->bal_cap < S) {
+    size_t scratch = 0;
+    int rc = lmoe_balance_scratch_bytes(&scratch);
+    if (rc) return rc;
+    Arena a;
+    float *ds, *loss, *part;
+    int* counts;
+    void* scr;
+    a.add((void**)&ds, Tm * E * 4);
+    a.add((void**)&part, (Tm + kAuxRows - 1) / kAuxRows * E * 4);
+    a.add((void**)&counts, (size_t)S * E * 4);
+    a.add((void**)&loss, 4);
+    a.add(&scr, scratch);
+    void* mem = nullptr;
+    if (cudaMalloc(&mem, a.off) != cudaSuccess) {
+      cudaGetLastError();
+      return LMOE_ENOMEM;
+    }
+    for (auto& it : a.items) *it.first = static_cast<uint8_t*>(mem) + it.second;
+    CK(cudaDeviceSynchronize());  // steps that use the old buffers
+    cudaFree(h->bal_mem);
+    h->bal_mem = mem;
+    h->bal_cap = S;
+    h->bal_ds = ds;
+    h->bal_part = part;
+    h->bal_counts = counts;
+    h->bal_loss = loss;
+    h->bal_scratch = scr;
+    CK(cudaMemset(h->bal_loss, 0, 4));
+    CK(cudaMemset(h->bal_counts, 0, (size_t)S * E * 4));
+  }
+  h->bal_on = coef != 0.f;
+  h->bal_coef = coef;
+  h->bal_cu = cu_seqlens;
+  h->bal_S = S;
+  h->g_bwd.reset(nullptr, nullptr, -1, 0, 0.f, 0);  // captured with the settings before
+  return LMOE_OK;
+}
+
+int lmoe_get_balance(lmoe_handle* h, float* loss, int32_t* counts, void* stream) {
+  if (!h || !h->bal_on) return LMOE_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (loss) CK(cudaMemcpyAsync(loss, h->bal_loss, 4, cudaMemcpyDeviceToDevice, st));
+  if (counts)
+    CK(cudaMemcpyAsync(counts, h->bal_counts, (size_t)h->bal_S * h->cfg.E * 4, cudaMemcpyDeviceToDevice, st));
   return LMOE_OK;
 }
 

@@ -79,8 +79,9 @@ def rmsnorm_backward(x: np.ndarray, gain: np.ndarray, eps: float, dx_hat: np.nda
     return dx, dgain
 
 
-def layer_backward(x, w: dict, b, k: int, dy, eps: float = 1e-6) -> dict:
-    """Gradients of sum(y * dy) for y = layer_forward(x, w, b, k, eps)["y"], in float64.
+def layer_backward(x, w: dict, b, k: int, dy, eps: float = 1e-6, dscores=None) -> dict:
+    """Gradients of sum(y * dy) for y = layer_forward(x, w, b, k, eps)["y"], in float64; dscores [T, E]:
+    the gradient of a further loss in the scores, added to theirs.
 
     Returns dx and one entry per weight of `w` (rms_gain, w_down, w_router, router_bias, w1, w3,
     w2, w_up, and ws1, ws3, ws2 when the shared expert exists), each of its weight's shape, plus
@@ -122,6 +123,8 @@ def layer_backward(x, w: dict, b, k: int, dy, eps: float = 1e-6) -> dict:
     # gates -> chosen scores -> router logits (unchosen scores get nothing)
     ds = np.zeros_like(s)
     ds[rows, idx] = gate_backward(s[rows, idx], dg)
+    if dscores is not None:
+        ds += f64(dscores)
     grads["w_router"], grads["router_bias"], dh_router = router_backward(ds, s, h, w_r)
     dh += dh_router
     # latent down-projection and RMSNorm

@@ -10,7 +10,10 @@ import numpy as np
 import pytest
 import torch
 
+import datagen
 import latent_routing_quantile_b200 as lq
+import oracle
+import oracle.backward
 import oracle.balance as ob
 
 pytestmark = pytest.mark.gpu
@@ -118,14 +121,15 @@ def test_no_tokens():
 def test_nan_scores_bad_experts_and_bad_bounds_are_reported():
     T, E, k = 40, 64, 4
     s, idx = inputs(T, E, k, 5)
-    bad = s.clone()
-    bad[9, 3] = float("nan")
-    out = lq.balance_loss(bad.cuda(), idx.cuda(), 0.1)
-    assert lq.op_status() == lq.STATUS_NAN_SCORE
-    assert torch.isnan(out["loss"]).all() and torch.isnan(out["dscores"][9]).all()
-    g = out["dscores"].cpu()
-    keep = torch.arange(T) != 9
-    assert torch.isfinite(g[keep]).all()
+    for v in (float("nan"), float("inf")):
+        bad = s.clone()
+        bad[9, 3] = v
+        out = lq.balance_loss(bad.cuda(), idx.cuda(), 0.1)
+        assert lq.op_status() == lq.STATUS_NAN_SCORE
+        assert torch.isnan(out["loss"]).all() and torch.isnan(out["dscores"][9]).all()
+        g = out["dscores"].cpu()
+        keep = torch.arange(T) != 9
+        assert torch.isfinite(g[keep]).all()
     wrong = idx.clone()
     wrong[2, 0], wrong[5, 1] = E, -7
     out = lq.balance_loss(s.cuda(), wrong.cuda(), 0.1)
@@ -172,3 +176,103 @@ def test_repeats_streams_and_graph_replay():
     s.copy_(dev[2][0]); i.copy_(dev[2][1])
     g.replay()
     assert same(out, ref[2])
+
+
+# ------------------------------------------------------------------ in the training step
+def train_layer(shape, w_dev):
+    return lq.Layer(shape.d, shape.l, shape.E, shape.k, shape.h, shape.hs, lq.BF16, shape.T, w_dev, rms_eps=shape.rms_eps)
+
+
+def train_reference(shape, w, x, dy, cu, coef):
+    r = oracle.layer_routing(x, w, np.zeros(shape.E), shape.k, shape.rms_eps)
+    cnt = ob.counts(r["idx"], shape.E, cu)
+    ds, _ = ob.gradient(r["s"], cnt, shape.k, cu, coef)
+    return (oracle.backward.layer_backward(x, w, np.zeros(shape.E), shape.k, dy, shape.rms_eps, dscores=ds),
+            ob.loss(r["s"], cnt, shape.k, cu, coef), cnt)
+
+
+def check_train(grads, ref, names=("x", "w_router", "router_bias", "w_down", "rms_gain", "w_up")):
+    """As for the backward's other gradients: at most 8 bf16 roundings on the longest chain, 2e-2 of the
+    largest magnitude."""
+    for n in names:
+        err = np.abs(grads[n].cpu().double().numpy() - ref[n]).max() / np.abs(ref[n]).max()
+        assert err <= 2e-2, (n, err)
+
+
+@pytest.mark.parametrize("T,E,k,cu", [(300, 64, 4, None), (300, 128, 6, [0, 130, 130, 290]), (1, 64, 4, None),
+                                      (200, 64, 4, [7, 150])])
+def test_training_step_with_a_balance_loss(T, E, k, cu):
+    """The weight makes the balance gradient as large as the rest of the router's (so that one left out, or
+    taken twice, fails)."""
+    shape = datagen.LayerShape("bal_train", T, 256, 128, E, k, 128, 256, "bf16", seed=91, offset_var=0.5)
+    w = datagen.layer_weights(shape, gain="random")
+    x, dy = datagen.tokens(shape), datagen.output_grad(shape, seed=191)
+    w_dev = {n: t.cuda() for n, t in w.items()}
+    layer = train_layer(shape, w_dev)
+    y0, g0 = layer.forward_backward(x.cuda(), dy.cuda(), w_dev)
+    bounds = [0, T] if cu is None else cu
+    coef = 20.0 * T
+    ref, loss, cnt = train_reference(shape, w, x, dy, bounds, coef)
+    layer.set_balance(coef, None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    y, g = layer.forward_backward(x.cuda(), dy.cuda(), w_dev)
+    got_loss, got_cnt = layer.balance()
+    assert torch.equal(y, y0)
+    assert np.array_equal(got_cnt.cpu().numpy(), cnt)
+    assert abs(float(got_loss) - loss) <= 1e-4 * loss  # the scores are within 2e-6 of the oracle's
+    check_train(g, ref)
+    assert (g["w_router"] - g0["w_router"]).norm() > 0.05 * g0["w_router"].norm()
+    for n in ("w1", "w3", "w2", "w_up", "ws2"):
+        # nothing on the experts' side of the choice changes (sums over K ranges may differ in the last bits)
+        assert torch.allclose(g[n], g0[n], rtol=1e-4, atol=1e-4 * float(g0[n].abs().max())), n
+    layer.set_balance(0.0)
+    _, g1 = layer.forward_backward(x.cuda(), dy.cuda(), w_dev)
+    for n in ("x", "w_router", "router_bias"):
+        assert torch.allclose(g1[n], g0[n], rtol=1e-4, atol=1e-4 * float(g0[n].abs().max())), n
+    with pytest.raises(lq.LmoeError):
+        layer.balance()
+    assert layer.status() == 0
+    layer.close()
+
+
+def test_training_steps_replay_with_new_bounds_and_more_sequences():
+    shape = datagen.LayerShape("bal_replay", 256, 256, 128, 64, 4, 128, 0, "bf16", seed=92, offset_var=0.5)
+    w = datagen.layer_weights(shape)
+    x, dy = datagen.tokens(shape), datagen.output_grad(shape, seed=192)
+    w_dev, xd, dyd = {n: t.cuda() for n, t in w.items()}, x.cuda(), dy.cuda()
+    layer = train_layer(shape, w_dev)
+    cu = torch.tensor([0, 100, 256], dtype=torch.int32, device="cuda")
+    layer.set_balance(3000.0, cu)
+    y, g = layer.forward_backward(xd, dyd, w_dev)
+    for _ in range(3):  # eager, captured, replayed
+        layer.forward_backward(xd, dyd, w_dev, y=y, grads=g)
+    check_train(g, train_reference(shape, w, x, dy, [0, 100, 256], 3000.0)[0])
+    cu.copy_(torch.tensor([0, 31, 200], dtype=torch.int32))  # other bounds, same graph
+    layer.forward_backward(xd, dyd, w_dev, y=y, grads=g)
+    check_train(g, train_reference(shape, w, x, dy, [0, 31, 200], 3000.0)[0])
+    five = [0, 50, 100, 150, 200, 256]
+    layer.set_balance(1000.0, torch.tensor(five, dtype=torch.int32, device="cuda"))
+    layer.forward_backward(xd, dyd, w_dev, y=y, grads=g)
+    ref, loss, cnt = train_reference(shape, w, x, dy, five, 1000.0)
+    check_train(g, ref)
+    assert np.array_equal(layer.balance()[1].cpu().numpy(), cnt)
+    assert layer.status() == 0
+    # bounds that do not fit the step: reported, and no balance loss
+    layer.set_balance(1000.0, torch.tensor([0, 300], dtype=torch.int32, device="cuda"))
+    layer.forward_backward(xd, dyd, w_dev, y=y, grads=g)
+    assert layer.status() == lq.STATUS_BAD_INDEX
+    check_train(g, oracle.backward.layer_backward(x, w, np.zeros(64), 4, dy, shape.rms_eps))
+    layer.close()
+
+
+def test_training_balance_is_refused_where_there_is_no_training():
+    shape = datagen.LayerShape("bal_mx", 64, 256, 128, 64, 4, 128, 256, "bf16", seed=74)
+    layer = lq.layer_from_weights(shape, datagen.layer_weights(shape), experts=lq.EXPERTS_MXFP4)
+    with pytest.raises(lq.LmoeError, match="unsupported"):
+        layer.set_balance(0.1)
+    layer.close()
+    layer = lq.layer_from_weights(shape, datagen.layer_weights(shape))
+    with pytest.raises(lq.LmoeError, match="invalid"):
+        layer.set_balance(float("nan"))
+    layer.set_balance(0.0, torch.zeros(100, dtype=torch.int32, device="cuda"))  # off: nothing is kept of it
+    layer.set_balance(0.1, torch.tensor([0, 64], dtype=torch.int32, device="cuda"))
+    layer.close()
