@@ -58,7 +58,7 @@ struct Mx4Cfg {
   static constexpr int kStages = BN == 128 ? 6 : 4;
   static constexpr int kStgOffset = kStages * kStageBytes;
   static constexpr int kBarOffset = kStgOffset + kMx4StgBytes;
-  static constexpr int kTableOffset = kBarOffset + 8 * (3 * kStages + 6) + 16;
+  static constexpr int kTableOffset = kBarOffset + 8 * (4 * kStages + 6) + 16;
   static constexpr int kSmemBytes = kTableOffset + 4 * kMx4TableInts;
   // TMEM columns: accumulators at 0 and 128, then the scales of each stage (A's 8 columns, B's BN / 16)
   static constexpr int kAcc1 = 128, kSfCols = 128 + BN, kSfBuf = 8 + BN / 16;
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
   uint64_t* empty = full + S;
-  uint64_t* sfull = empty + S;  // the stage's scales are in TMEM
+  uint64_t* sload = empty + S;  // the stage's scale atoms are in shared memory
+  uint64_t* sfull = sload + S;  // ... and in TMEM
   uint64_t* tfull = sfull + S;
   uint64_t* tempty = tfull + 2;
   uint64_t* tovl = tempty + 2;  // the shared columns of the tile before have been read
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&sload[i], 1);
       mbar_init(&sfull[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -269,9 +271,11 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
           uint8_t* a_dst = smem + stage * C::kStageBytes;
           uint8_t* b_dst = a_dst + C::kABytes;
           uint8_t* s_dst = b_dst + C::kBBytes;
-          mbar_expect_tx(&full[stage], C::kStageBytes - (few ? 96 * 128 : 0));
-          tma_load_3d(s_dst, &p.tmSA, &full[stage], 0, kb * 8, mt);
-          tma_load_3d(s_dst + 1024, &p.tmSB, &full[stage], 0, kb * 8, sb0);
+          // the scales first, on a barrier of their own: they are in TMEM before the tiles are here
+          mbar_expect_tx(&sload[stage], 1024 + C::kSBBytes);
+          tma_load_3d(s_dst, &p.tmSA, &sload[stage], 0, kb * 8, mt);
+          tma_load_3d(s_dst + 1024, &p.tmSB, &sload[stage], 0, kb * 8, sb0);
+          mbar_expect_tx(&full[stage], C::kABytes + C::kBBytes - (few ? 96 * 128 : 0));
           tma_load_2d(a_dst, few ? &p.tmA32 : &p.tmA, &full[stage], kb * 128, row0);
           tma_load_2d(b_dst, &p.tmB, &full[stage], kb * 128, brow0);
           if constexpr (BN == 256) tma_load_2d(b_dst + 16384, &p.tmB, &full[stage], kb * 128, brow0 + 128);
@@ -287,7 +291,10 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     }
     if (!ok && lane == 0)
       for (int i = 0; i < S; ++i)
-        if ((armed >> i) & 1u) mbar_drain(&full[i], (armed_parity >> i) & 1u);
+        if ((armed >> i) & 1u) {
+          mbar_drain(&full[i], (armed_parity >> i) & 1u);
+          mbar_drain(&sload[i], (armed_parity >> i) & 1u);
+        }
   } else if (warp == 1) {
     if (lane == 0) {
       // ---------------- MMA issuer
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     bool ok = true;
     for (int tile = first; ok && tile < num_tiles; tile += stride) {
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = mbar_wait(&full[stage], phase, abort, p.status);
+        ok = mbar_wait(&sload[stage], phase, abort, p.status);
         __syncwarp();
         if (__any_sync(0xffffffffu, !ok)) {
           ok = false;
