@@ -43,6 +43,7 @@ sys.path.insert(0, ROOT)
 METRIC = "LatentMoE layer fwd tokens/s on 1 B200; % BF16 tensor peak; router/permute GB/s"
 UNIT = "tokens/s"
 BETA = 0.01
+EXPERT_FORMATS = {"bf16": 0, "mxfp8": 1, "mxfp4": 4}  # the binding's EXPERTS_* values
 FLUSH_BYTES = 256 << 20
 FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustained": 1400.0}
 
@@ -302,8 +303,9 @@ def measure(shape, args, rank, world, local_rank, e2e=True, experts=0):
     rpc_ms = sum(per_launch[n] for n in rpc)
     ex_flops = work["expert_swiglu"][0] + work["expert_down"][0]
     ex_ms = per_launch["expert_swiglu"] + per_launch["expert_down"]
-    # 8-bit experts run at twice the bf16 tensor rate (the dense fp8 rate is twice bf16's)
-    ex_peak = peaks["bf16_tflops"] * (2 if experts else 1)
+    # 8-bit experts run at twice the bf16 tensor rate (the dense fp8 rate is twice bf16's), 4-bit ones at
+    # four times
+    ex_peak = peaks["bf16_tflops"] * {0: 1, 1: 2, 4: 4}[experts]
     summary = {
         "workload": shape.name, "T": T, "ms_per_step": round(ms_max, 5),
         "value": round(T * world / (ms_max / 1e3), 1),
@@ -316,7 +318,7 @@ def measure(shape, args, rank, world, local_rank, e2e=True, experts=0):
         "expert_gemm_frac_of_bf16_peak": round(ex_flops / (ex_ms / 1e3) / 1e12 / peaks["bf16_tflops"], 4),
         "expert_gemm_tflops": round(ex_flops / (ex_ms / 1e3) / 1e12, 1),
         "expert_gemm_frac_of_format_peak": round(ex_flops / (ex_ms / 1e3) / 1e12 / ex_peak, 4),
-        "experts": "mxfp8" if experts else "bf16",
+        "experts": next(f for f, n in EXPERT_FORMATS.items() if n == experts),
         "clocks": clk.summary(),
         "e2e_ms": e2e_ms, "e2e_steps": e2e_steps, "stage_ms": per_launch, "work": work,
         "peaks": (peaks, peak_src),
@@ -418,7 +420,7 @@ def run_ours(args, rank, world, local_rank):
     shape = datagen.WORKLOADS[args.workload]
     if args.tokens:
         shape = shape.with_tokens(args.tokens)
-    main_s, launches = measure(shape, args, rank, world, local_rank, experts=1 if args.experts == "mxfp8" else 0)
+    main_s, launches = measure(shape, args, rank, world, local_rank, experts=EXPERT_FORMATS[args.experts])
     also, train = {}, {}
     if world == 1 and args.also and not args.tokens:
         for spec in args.also.split(","):
@@ -427,9 +429,9 @@ def run_ours(args, rank, world, local_rank):
             if len(parts) > 2 and parts[2] == "train":
                 train[sh.name] = measure_train(sh, args, local_rank)
                 continue
-            mx = len(parts) > 2 and parts[2] == "mxfp8"
-            s2, _ = measure(sh, args, rank, world, local_rank, e2e=False, experts=1 if mx else 0)
-            also[sh.name + ("_mxfp8" if mx else "")] = s2
+            fmt = parts[2] if len(parts) > 2 else "bf16"
+            s2, _ = measure(sh, args, rank, world, local_rank, e2e=False, experts=EXPERT_FORMATS[fmt])
+            also[sh.name + ("" if fmt == "bf16" else "_" + fmt)] = s2
     if rank != 0:
         return None
     m = main_s
@@ -585,10 +587,10 @@ def main():
     ap.add_argument("--workload", default="wide_stress")
     ap.add_argument("--tokens", type=int, default=0)
     ap.add_argument("--also", default="sweep:262144,wide_stress:16384:mxfp8,mini_replica:8192:train",
-                    help="extra workloads (name:T[:mxfp8|:train], comma-separated) measured in the same call on one "
-                         "GPU, ':mxfp8' with 8-bit routed experts, ':train' as training steps (forward + backward); "
+                    help="extra workloads (name:T[:mxfp8|:mxfp4|:train], comma-separated) measured in the same call on one "
+                         "GPU, ':mxfp8' and ':mxfp4' with 8-bit and 4-bit routed experts, ':train' as training steps (forward + backward); "
                          "'' for none")
-    ap.add_argument("--experts", choices=["bf16", "mxfp8"], default="bf16",
+    ap.add_argument("--experts", choices=list(EXPERT_FORMATS), default="bf16",
                     help="operand format of the routed experts of the main workload")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--train-only", default="",
