@@ -88,18 +88,22 @@ int launch_mx4_gemm(const Mx4GemmParams& p, int grid, cudaStream_t st) {
   return LMOE_OK;
 }
 
-// How a product is cut (see mx4_gemm.cuh).
+// How a product is cut (see mx4_gemm.cuh): tile width, CTAs a tile, grid.
 struct Mx4Plan {
   int bn, split, grid;
 };
 Mx4Plan plan_mx4(int M, int N, int nkb, int groups, bool ragged, int sms) {
   const long long mt = work_tiles(M, groups, ragged);
   const long long t128 = mt * ((N + 127) / 128), t256 = mt * ((N + 255) / 256);
-  // 256-wide tiles where they take fewer waves of the GPU by more than their longer k-blocks cost
+  // 256-wide tiles where they take at most two thirds of the 128-wide ones' waves: 2048 x 2048 x 2048,
+  // one wave for two, 8.1 us against 10.6; 16384 x 8192 x 7168 356 against 560; one token's 16 experts,
+  // one wave either way, 8.8 against 7.8
   if ((t256 + sms - 1) / sms * 3 <= (t128 + sms - 1) / sms * 2)
     return {256, 1, (int)std::min<long long>(t256, sms)};
-  // too few tiles for the GPU and a long K: clusters share them (eight CTAs only while half the GPU
-  // holds them all, since not every SM has seven neighbours free)
+  // too few tiles for the GPU and a K of 12 k-blocks or more: clusters share the tiles (1 x 1024 x 7168
+  // 12.0 us alone, 7.0 in fours, 6.3 in eights; 1 x 7168 x 2048, eight k-blocks, 6.2 alone, 6.5 in twos).
+  // Eight CTAs only while half the GPU holds them all, since not every SM has seven neighbours free
+  // (16 tiles of 2048 x 4096: 19.6 us in eights, 8.5 in fours)
   int split = 1;
   if (nkb >= 12)
     while (split < 8 && nkb >= 8 * split && 2 * split * t128 <= (split < 4 ? sms : sms / 2)) split *= 2;
