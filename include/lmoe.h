@@ -412,7 +412,7 @@ int lmoe_mx4_gemm(const uint8_t *a_elems, const uint8_t *a_scales, const uint8_t
  * score makes the loss and its token's gradient NaN and sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index
  * other than -1 outside [0, E) is not counted, and it, or cu_seqlens that decrease or leave [0, T],
  * sets LMOE_STATUS_BAD_INDEX (the bits are ORed in, never cleared).
- * E at most 1024, k at most 32.  scratch is lmoe_balance_scratch_bytes of device memory, 16-byte
+ * E at most 1024, k at most 32, S at most 2^24, T k at most 2^30.  scratch is lmoe_balance_scratch_bytes of device memory, 16-byte
  * aligned, the call's own until it has run.  Sums are taken in a fixed order: the same call gives
  * the same bits every time. */
 int lmoe_balance_scratch_bytes(size_t *bytes);

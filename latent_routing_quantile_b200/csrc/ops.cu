@@ -39,6 +39,9 @@ long long work_tiles(int64_t rows, int32_t groups, bool ragged) {
   return ragged ? rows / 128 + std::min<int64_t>(groups, rows) : scale_tiles(rows, groups, false);
 }
 
+// Words the kernels read or add to: not null (unless it may be), on a 4-byte boundary.
+bool words(const void* p, bool optional = false) { return (p || optional) && ((uintptr_t)p & 3) == 0; }
+
 // Widest access that every row of a matrix allows (rows `ld` elements apart).
 int row_access(const void* p, int64_t ld, int32_t dtype) {
   const uint64_t a = (uint64_t)(uintptr_t)p | (uint64_t)(ld * (dtype == LMOE_F32 ? 4 : 2));
@@ -161,9 +164,9 @@ int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, const int32_t* inde
   if (dtype != LMOE_F32 && dtype != LMOE_BF16) return LMOE_EINVAL;
   if (index && (x_rows < 0 || x_rows > INT32_MAX)) return LMOE_EINVAL;
   if (rows == 0) return LMOE_OK;
-  if (!x || !elems || !scales || !status || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
-    return LMOE_EINVAL;
-  if ((uintptr_t)x % (dtype == LMOE_F32 ? 4 : 2) || (uintptr_t)index % 4) return LMOE_EINVAL;
+  if (!x || !elems || !scales || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15)) return LMOE_EINVAL;
+  if (!words(status) || !words(offsets, true) || !words(index, true)) return LMOE_EINVAL;
+  if ((uintptr_t)x % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
   int sms = 0;
   const int drc = device_sms(&sms);
   if (drc) return drc;
@@ -200,7 +203,7 @@ int lmoe_mx4_quant_w13(const void* w1, const void* w3, int32_t dtype, int32_t gr
   const int rc = check_rows(rows, cols, groups, false);
   if (rc) return rc;
   if (dtype != LMOE_F32 && dtype != LMOE_BF16) return LMOE_EINVAL;
-  if (!w1 || !w3 || !elems || !scales || !status || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
+  if (!w1 || !w3 || !elems || !scales || !words(status) || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
     return LMOE_EINVAL;
   if (((uintptr_t)w1 | (uintptr_t)w3) % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
   int sms = 0;
@@ -233,8 +236,8 @@ int lmoe_mx4_dequant(const uint8_t* elems, const uint8_t* scales, int64_t rows, 
   if (rc) return rc;
   if ((dtype != LMOE_F32 && dtype != LMOE_BF16) || (flags & ~LMOE_MX4_ZERO_REST)) return LMOE_EINVAL;
   if (rows == 0) return LMOE_OK;
-  if (!out || !elems || !scales || !status || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15))
-    return LMOE_EINVAL;
+  if (!out || !elems || !scales || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15)) return LMOE_EINVAL;
+  if (!words(status) || !words(offsets, true)) return LMOE_EINVAL;
   if ((uintptr_t)out % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
   int sms = 0;
   const int drc = device_sms(&sms);
@@ -273,7 +276,8 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   if (swiglu && (N % 128 || c_dtype != LMOE_BF16)) return LMOE_EUNSUPPORTED;
   if (M == 0) return LMOE_OK;
   const int32_t cols = swiglu ? N / 2 : N;
-  if (!a_elems || !a_scales || !b_elems || !b_scales || !c || !status || ldc < cols) return LMOE_EINVAL;
+  if (!a_elems || !a_scales || !b_elems || !b_scales || !c || ldc < cols) return LMOE_EINVAL;
+  if (!words(status) || !words(offsets, true)) return LMOE_EINVAL;
   if (((uintptr_t)a_elems | (uintptr_t)a_scales | (uintptr_t)b_elems | (uintptr_t)b_scales) & 15) return LMOE_EINVAL;
   if ((uintptr_t)c % (c_dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
   int sms = 0;
@@ -323,10 +327,9 @@ int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_
                       const int32_t* cu_seqlens, int32_t S, float coef, int32_t* counts, float* loss, float* dscores,
                       void* scratch, uint32_t* status, void* stream) {
   if (T < 0 || E <= 0 || k <= 0 || k > E || S <= 0 || (!cu_seqlens && S != 1) || !(coef == coef)) return LMOE_EINVAL;
-  if (E > 1024 || k > 32 || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
-  if (!counts || !loss || !scratch || !status || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
-  if (T && (!scores || !idx)) return LMOE_EINVAL;
-  if (((uintptr_t)scores | (uintptr_t)dscores | (uintptr_t)idx | (uintptr_t)counts | (uintptr_t)loss) & 3)
+  if (E > 1024 || k > 32 || S > (1 << 24) || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
+  if (!words(counts) || !words(loss) || !words(status) || !scratch || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
+  if (!words(scores, T == 0) || !words(idx, T == 0) || !words(dscores, true) || !words(cu_seqlens, true))
     return LMOE_EINVAL;
   int sms = 0;
   const int rc = device_sms(&sms);

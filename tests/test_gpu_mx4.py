@@ -104,12 +104,16 @@ def test_quant_special_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("pitch,first", [(160, 0), (161, 0), (200, 3), (164, 4)])
+@pytest.mark.parametrize("pitch,first", [(160, 0), (161, 0), (200, 3), (164, 4), (168, 8)])
 def test_quant_strided_and_misaligned_rows(dtype, pitch, first):
     base = rows((70, pitch + 8), 3, dtype).cuda()
     x = base[:, first:first + 160]
     q = lq.mx4_quant(x)
     assert np.array_equal(np64(lq.mx4_dequant(q, dtype=torch.float32)), mx.values(np64(x)))
+    for dt in (torch.bfloat16, torch.float32):
+        for at in (1, 4, 8):  # off every boundary, and on 8, 16 and 32 bytes
+            out = torch.empty(70 * 160 + at, dtype=dt, device="cuda")[at:].view(70, 160)
+            assert np.array_equal(np64(lq.mx4_dequant(q, out=out)), mx.values(np64(x)))
 
 
 @pytest.mark.parametrize("head,sizes,tail", [(0, [5, 0, 130, 1, 0, 256], 0), (3, [1, 1, 1], 9), (0, [0, 0], 4),
@@ -336,6 +340,38 @@ def test_streams_and_graph_replay():
     o.copy_(ragged(300, [0, 300, 0, 0]))
     g.replay()
     assert torch.equal(y, lq.mx4_gemm(lq.mx4_quant(a[3], offsets=o), b))
+
+
+def test_two_graphs_at_once_and_alternating():
+    """Two captured graphs of the operators, replayed on two streams at the same time and in turn: they share
+    no workspace."""
+    ws = [lq.mx4_quant(rows((256, 4128), 90 + i, spread=1).cuda()) for i in range(2)]
+    xs = [rows((70, 4128), 95 + i).cuda() for i in range(2)]  # K split over clusters
+    ss = [torch.sigmoid(torch.randn(400, 64, generator=torch.Generator().manual_seed(i))).cuda() for i in range(2)]
+    ids = [s.topk(4, dim=1).indices.int() for s in ss]
+    once = lambda i: (lq.mx4_gemm(lq.mx4_quant(xs[i]), ws[i], dtype=torch.float32),
+                      *lq.balance_loss(ss[i], ids[i], 0.1).values())
+    ref = [once(0), once(1)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(once(i))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], ref[i]))
+    for i in (1, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], ref[i]))
 
 
 def test_experts_after_routing():

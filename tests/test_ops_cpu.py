@@ -113,7 +113,7 @@ P = 1 << 20  # a pointer that is aligned and never read
     (dict(cols=33), EUNSUPPORTED), (dict(rows=-1), EINVAL), (dict(groups=0), EINVAL), (dict(dtype=2), EINVAL),
     (dict(ld=63), EINVAL), (dict(x=None), EINVAL), (dict(x=P + 1), EINVAL), (dict(elems=P + 8), EINVAL),
     (dict(scales=None), EINVAL), (dict(status=None), EINVAL), (dict(groups=2, rows=5), EINVAL), (dict(rows=0), 0),
-    (dict(index=P + 2), EINVAL), (dict(index=P, x_rows=-1), EINVAL), (dict(index=P, x_rows=1 << 31), EINVAL),
+    (dict(status=P + 2), EINVAL), (dict(offsets=P + 1), EINVAL), (dict(index=P + 2), EINVAL), (dict(index=P, x_rows=-1), EINVAL), (dict(index=P, x_rows=1 << 31), EINVAL),
     (dict(rows=1 << 30, cols=1 << 20, ld=1 << 20), EUNSUPPORTED)])
 def test_quant_refusals(L, change, code):
     a = dict(x=P, dtype=1, ld=64, index=None, x_rows=0, rows=4, cols=64, groups=1, offsets=None, elems=P, scales=P,
@@ -133,7 +133,8 @@ def test_quant_w13_refusals(L, change, code):
 
 @pytest.mark.parametrize("change,code", [
     (dict(cols=33), EUNSUPPORTED), (dict(dtype=2), EINVAL), (dict(ld=32), EINVAL), (dict(out=P + 1), EINVAL),
-    (dict(flags=1), EINVAL), (dict(elems=None), EINVAL), (dict(rows=0), 0)])
+    (dict(flags=1), EINVAL), (dict(elems=None), EINVAL), (dict(status=P + 1), EINVAL), (dict(offsets=P + 2), EINVAL),
+    (dict(rows=0), 0)])
 def test_dequant_refusals(L, change, code):
     a = dict(elems=P, scales=P, rows=4, cols=64, groups=1, offsets=None, out=P, dtype=1, ld=64, flags=0, status=P,
              stream=None)
@@ -145,7 +146,7 @@ def test_dequant_refusals(L, change, code):
     (dict(K=48), EUNSUPPORTED), (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(groups=2), EINVAL),
     (dict(flags=4), EINVAL), (dict(flags=1, N=64), EUNSUPPORTED), (dict(flags=1, N=128, dtype=0), EUNSUPPORTED),
     (dict(ldc=7), EINVAL), (dict(c=P + 1), EINVAL), (dict(c=P + 2, dtype=0), EINVAL), (dict(b_scales=P + 8), EINVAL),
-    (dict(status=None), EINVAL), (dict(groups=1000, offsets=P, N=1 << 21), EUNSUPPORTED), (dict(M=0), 0)])
+    (dict(status=None), EINVAL), (dict(status=P + 2), EINVAL), (dict(offsets=P + 1), EINVAL), (dict(groups=1000, offsets=P, N=1 << 21), EUNSUPPORTED), (dict(M=0), 0)])
 def test_gemm_refusals(L, change, code):
     a = dict(a_elems=P, a_scales=P, b_elems=P, b_scales=P, M=4, N=8, K=64, groups=1, offsets=None, c=P, dtype=1,
              ldc=64, flags=0, status=P, stream=None)
@@ -156,7 +157,8 @@ def test_gemm_refusals(L, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(E=1025), EUNSUPPORTED), (dict(k=33, E=64), EUNSUPPORTED), (dict(k=9), EINVAL), (dict(T=-1), EINVAL),
     (dict(S=2), EINVAL), (dict(S=0), EINVAL), (dict(coef=float("nan")), EINVAL), (dict(counts=None), EINVAL),
-    (dict(scratch=P + 8), EINVAL), (dict(scores=P + 2), EINVAL), (dict(idx=None), EINVAL), (dict(status=None), EINVAL)])
+    (dict(scratch=P + 8), EINVAL), (dict(scores=P + 2), EINVAL), (dict(idx=None), EINVAL), (dict(status=None), EINVAL),
+    (dict(status=P + 1), EINVAL), (dict(cu=P + 2, S=2), EINVAL), (dict(S=(1 << 24) + 1, cu=P), EUNSUPPORTED)])
 def test_balance_refusals(L, change, code):
     a = dict(scores=P, idx=P, T=4, E=8, k=2, cu=None, S=1, coef=0.1, counts=P, loss=P, dscores=P, scratch=P, status=P,
              stream=None)
