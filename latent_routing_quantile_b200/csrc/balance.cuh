@@ -83,11 +83,11 @@ __device__ __forceinline__ BalSeqs bal_seqs(const BalanceParams& p, BalSeqSmem& 
   return BalSeqs{p.S <= kBalSeqCache ? m.cu : p.cu, m.bad ? 0 : p.S, m.filled};
 }
 
-// Copies of each of n shared counters: a power of two up to 32, one a lane where there is room, so that
-// few experts' counters do not make the lanes wait for each other.
+// Copies of each of n shared counters: a power of two up to 32, one a lane where there are few, so that
+// few experts' counters do not make the lanes wait for each other (many experts' hardly meet).
 __device__ __forceinline__ int bal_copies(int n) {
   int c = 32;
-  while (c > 1 && n * c > kBalHistInts) c >>= 1;
+  while (c > 1 && n * c > 4096) c >>= 1;
   return c;
 }
 // Adds the choices of tokens [lo, hi) to hist (copies of each expert side by side).
