@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblmoe.so")
 SOURCES = ["lmoe.cu", "ops.cu"]
-HEADERS = ["balance.cuh", "bwd.cuh", "common.cuh", "host.cuh", "k1_router.cuh", "mx4.cuh", "mx4_gemm.cuh", "q8_gemm.cuh", "route.cuh", "tc_gemm.cuh"]
+HEADERS = ["balance.cuh", "bwd.cuh", "common.cuh", "host.cuh", "k1_router.cuh", "mx4.cuh", "mx4_gemm.cuh",
+           "q8_gemm.cuh", "route.cuh", "tc_gemm.cuh"]
 
 
 def nvcc() -> str:

@@ -21,9 +21,11 @@
 // ring itself (they released the stage before it was loaded again).
 //
 // Measured: 16384 x 8192 x 7168 with the SwiGLU epilogue 356 us, 5.4 PFLOP/s (the MMAs alone 290 us, the
-// loads alone 275); sustained, at the power cap's clock, 424 us.  The wide layer's gate and linear
-// projections (262144 rows over 896 experts, 1024 x 2048) 344 us: MMAs alone 220, a quarter of them
-// for the rows that fill up an expert's last tile, loads alone 224.
+// loads alone 275); sustained, at the power cap's clock, 424 us.  Together they are held by shared
+// memory: a k-block of a 128 x 256 tile writes 51 KB and reads 48 KB of it, 774 cycles at 128 bytes a
+// cycle, of the 890 that it takes.  The wide layer's gate and linear projections (262144 rows over 896
+// experts, 1024 x 2048) 344 us: MMAs alone 220, a quarter of them for the rows that fill up an expert's
+// last tile, loads alone 224.
 #pragma once
 
 #include "mx4.cuh"
@@ -33,7 +35,7 @@ namespace lmoe {
 struct Mx4GemmParams {
   CUtensorMap tmA;   // codes [M, K / 2] u8, box 128 bytes x 128 rows
   CUtensorMap tmA32; // the same, boxes of 32 rows (tiles of at most 32 rows)
-  CUtensorMap tmB;   // codes [groups N, K / 2] u8, box 128 bytes x 128 rows
+  CUtensorMap tmB;   // codes [groups N, K / 2] u8, box 128 bytes x the tile's width
   CUtensorMap tmSA;  // scale atoms, see make_map_atoms: one row tile a box
   CUtensorMap tmSB;  // one or two (256-wide tiles) row tiles a box
   CUtensorMap tmC;   // c, boxes of a staging round (mx4_store_rows); used when vec
@@ -283,7 +285,6 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
           mbar_expect_tx(&full[stage], C::kABytes + C::kBBytes - (few ? 96 * 128 : 0));
           tma_load_2d(a_dst, few ? &p.tmA32 : &p.tmA, &full[stage], kb * 128, row0);
           tma_load_2d(b_dst, &p.tmB, &full[stage], kb * 128, brow0);
-          if constexpr (BN == 256) tma_load_2d(b_dst + 16384, &p.tmB, &full[stage], kb * 128, brow0 + 128);
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {

@@ -289,7 +289,7 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   memset(&p, 0, sizeof(p));
   p.b_tiles = (N + 127) / 128;
   if (!make_map_u8(&p.tmA, a_elems, M, K / 2, K / 2, 128) || !make_map_u8(&p.tmA32, a_elems, M, K / 2, K / 2, 32) ||
-      !make_map_u8(&p.tmB, b_elems, (long long)groups * N, K / 2, K / 2, 128) ||
+      !make_map_u8(&p.tmB, b_elems, (long long)groups * N, K / 2, K / 2, plan.bn) ||
       !make_map_atoms(&p.tmSA, a_scales, scale_tiles(M, groups, offsets != nullptr), nkb, 1) ||
       !make_map_atoms(&p.tmSB, b_scales, (long long)groups * p.b_tiles, nkb, plan.bn / 128))
     return LMOE_ECUDA;
