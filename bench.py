@@ -587,8 +587,9 @@ def main():
     ap.add_argument("--workload", default="wide_stress")
     ap.add_argument("--tokens", type=int, default=0)
     ap.add_argument("--also", default="sweep:262144,wide_stress:16384:mxfp8,mini_replica:8192:train",
-                    help="extra workloads (name:T[:mxfp8|:mxfp4|:train], comma-separated) measured in the same call on one "
-                         "GPU, ':mxfp8' and ':mxfp4' with 8-bit and 4-bit routed experts, ':train' as training steps (forward + backward); "
+                    help="extra workloads (name:T[:mxfp8|:mxfp4|:train], comma-separated) measured in the same call "
+                         "on one GPU, ':mxfp8' and ':mxfp4' with 8-bit and 4-bit routed experts, ':train' as training "
+                         "steps (forward + backward); "
                          "'' for none")
     ap.add_argument("--experts", choices=list(EXPERT_FORMATS), default="bf16",
                     help="operand format of the routed experts of the main workload")

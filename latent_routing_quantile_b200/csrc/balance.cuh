@@ -191,7 +191,8 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
 // The pass over tokens [t0, t1), sequence by sequence (counts known): the block's share of the loss, for
 // thread 0.  f: shared, [E]; wsum: shared, [kBalThreads / 32] doubles.
 template <int NJ, int VEC, int R, int LANES>
-__device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs& sq, int t0, int t1, float* f, double* wsum) {
+__device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs& sq, int t0, int t1, float* f,
+                                           double* wsum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double acc = 0;
   bool nan = false;

@@ -504,7 +504,8 @@ int validate(const lmoe_config* c) {
     if (c->dtype != LMOE_BF16) return LMOE_EUNSUPPORTED;
     // the 4-bit calls' own limits on the weights and on the routed rows
     size_t e = 0, s = 0;
-    if (lmoe_mx4_bytes(2ll * c->E * c->h, c->l, c->E, 0, &e, &s) || lmoe_mx4_bytes((int64_t)c->E * c->l, c->h, c->E, 0, &e, &s) ||
+    if (lmoe_mx4_bytes(2ll * c->E * c->h, c->l, c->E, 0, &e, &s) ||
+        lmoe_mx4_bytes((int64_t)c->E * c->l, c->h, c->E, 0, &e, &s) ||
         lmoe_mx4_bytes((int64_t)c->max_tokens * c->k, std::max(c->l, c->h), c->E, 1, &e, &s))
       return LMOE_EUNSUPPORTED;
   }

@@ -9,7 +9,7 @@
 //
 // Elements are row-major, cols / 2 bytes a row.  Scales are stored as the tensor core reads them:
 // the scales of 128 rows and 128 columns (4 blocks) form a 512-byte atom, byte 16 i + 4 j + b = row
-// i + 32 j, block b (i < 32, j < 4, b < 4), which one tcgen05.cp copies into four TMEM columns.
+// i + 32 j, block b (i < 32, j < 4, b < 4): lane i of four TMEM columns, a word a lane and column.
 // Atoms are stored row tile by row tile, two per 256 columns (one k-block of the products).  Blocks
 // past the last column have scale byte 0: their elements read as zeros, and 0 times a finite scale
 // adds nothing.  Rows come in groups (one for a plain matrix, an expert's rows, an expert's weight
@@ -72,10 +72,9 @@ struct Mx4Tiles {
 
 constexpr int kMx4TableInts = (kMx4MaxGroups + 1) + (kMx4MaxGroups + 2) / 2 + 1 + 8;
 
-// Fills the tile table (at least 256 threads, every thread of the block takes part; ends with a
-// barrier).  Offsets that
-// decrease or leave [0, rows] are recorded as LMOE_STATUS_BAD_INDEX and give no tiles at all, so no
-// access follows from them (every row then belongs to no group).
+// Fills the tile table (at least 256 threads; every thread of the block takes part; ends with a
+// barrier).  Offsets that decrease or leave [0, rows] are recorded as LMOE_STATUS_BAD_INDEX and give no
+// tiles at all, so no access follows from them (every row then belongs to no group).
 __device__ inline Mx4Tiles mx4_tiles(const Mx4Rows& r, int* table, uint32_t* status) {
   Mx4Tiles t;
   t.groups = r.groups;

@@ -210,7 +210,8 @@ def test_product_into_strided_output_leaves_the_rest(out, pitch):
     assert (buf[0] == 7).all() and (buf[M + 1] == 7).all() and (buf[:, N:] == 7).all()
 
 
-GROUPS = [(0, [5, 0, 130, 1, 0, 256], 0), (3, [1, 1, 1], 9), (0, [0, 0], 4), (0, [200], 0), (2, [31, 33, 127, 128, 129], 1),
+GROUPS = [(0, [5, 0, 130, 1, 0, 256], 0), (3, [1, 1, 1], 9), (0, [0, 0], 4), (0, [200], 0),
+          (2, [31, 33, 127, 128, 129], 1),
           (0, [1] * 16, 0), (0, [300, 0, 0, 290, 310, 33, 600, 2], 0),
           (5, list(range(0, 270, 3)), 6)]  # 90 groups: 256-wide tiles at N >= 257
 
@@ -276,7 +277,8 @@ def test_blocks_of_nan_reach_their_rows_and_columns_only():
 
 
 def test_empty_and_bad_offsets():
-    assert lq.mx4_gemm(lq.mx4_quant(torch.empty(0, 64, device="cuda")), lq.mx4_quant(rows((8, 64), 1).cuda())).shape == (0, 8)
+    none = lq.mx4_quant(torch.empty(0, 64, device="cuda"))
+    assert lq.mx4_gemm(none, lq.mx4_quant(rows((8, 64), 1).cuda())).shape == (0, 8)
     x, w = rows((20, 64), 1).cuda(), lq.mx4_quant(rows((2, 8, 64), 1).cuda())
     for off in ([0, 12, 21], [0, 12, 5], [-1, 3, 20]):
         q = lq.mx4_quant(x, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))

@@ -113,7 +113,8 @@ P = 1 << 20  # a pointer that is aligned and never read
     (dict(cols=33), EUNSUPPORTED), (dict(rows=-1), EINVAL), (dict(groups=0), EINVAL), (dict(dtype=2), EINVAL),
     (dict(ld=63), EINVAL), (dict(x=None), EINVAL), (dict(x=P + 1), EINVAL), (dict(elems=P + 8), EINVAL),
     (dict(scales=None), EINVAL), (dict(status=None), EINVAL), (dict(groups=2, rows=5), EINVAL), (dict(rows=0), 0),
-    (dict(status=P + 2), EINVAL), (dict(offsets=P + 1), EINVAL), (dict(index=P + 2), EINVAL), (dict(index=P, x_rows=-1), EINVAL), (dict(index=P, x_rows=1 << 31), EINVAL),
+    (dict(status=P + 2), EINVAL), (dict(offsets=P + 1), EINVAL), (dict(index=P + 2), EINVAL),
+    (dict(index=P, x_rows=-1), EINVAL), (dict(index=P, x_rows=1 << 31), EINVAL),
     (dict(rows=1 << 30, cols=1 << 20, ld=1 << 20), EUNSUPPORTED)])
 def test_quant_refusals(L, change, code):
     a = dict(x=P, dtype=1, ld=64, index=None, x_rows=0, rows=4, cols=64, groups=1, offsets=None, elems=P, scales=P,
@@ -146,7 +147,8 @@ def test_dequant_refusals(L, change, code):
     (dict(K=48), EUNSUPPORTED), (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(groups=2), EINVAL),
     (dict(flags=4), EINVAL), (dict(flags=1, N=64), EUNSUPPORTED), (dict(flags=1, N=128, dtype=0), EUNSUPPORTED),
     (dict(ldc=7), EINVAL), (dict(c=P + 1), EINVAL), (dict(c=P + 2, dtype=0), EINVAL), (dict(b_scales=P + 8), EINVAL),
-    (dict(status=None), EINVAL), (dict(status=P + 2), EINVAL), (dict(offsets=P + 1), EINVAL), (dict(groups=1000, offsets=P, N=1 << 21), EUNSUPPORTED), (dict(M=0), 0)])
+    (dict(status=None), EINVAL), (dict(status=P + 2), EINVAL), (dict(offsets=P + 1), EINVAL),
+    (dict(groups=1000, offsets=P, N=1 << 21), EUNSUPPORTED), (dict(M=0), 0)])
 def test_gemm_refusals(L, change, code):
     a = dict(a_elems=P, a_scales=P, b_elems=P, b_scales=P, M=4, N=8, K=64, groups=1, offsets=None, c=P, dtype=1,
              ldc=64, flags=0, status=P, stream=None)
