@@ -161,7 +161,7 @@ def prepare(case, seed):
         import latent_routing_quantile_b200 as lq
         if case["swiglu"]:
             v = w.view(w.shape[0], N // 128, 2, 64, K)
-            w1, w3 = v[:, :, 0].reshape(-1, N // 2, K), v[:, :, 1].reshape(-1, N // 2, K)
+            w1, w3 = (v[:, :, i].reshape(-1, N // 2, K).contiguous() for i in range(2))
             s["w"] = lq.mx4_quant_w13(w1, w3) if op == "grouped" else lq.mx4_quant_w13(w1[0], w3[0])
         else:
             s["w"] = lq.mx4_quant(w if op == "grouped" else w[0])
