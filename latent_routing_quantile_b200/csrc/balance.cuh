@@ -9,6 +9,8 @@
 //   dL/ds_te = w_q (f_qe - D_t) / R_t.
 // With the counts known, the loss and its gradient need one pass over the scores: the mean
 // probabilities are never formed.  The pass is bound by memory (scores read, gradient written).
+// Near balance f and D are both close to 1 and f - D cancels, so both are held as what they differ from
+// 1 by, f from whole numbers: f_qe - 1 = (counts_qe E - k n_q) / (k n_q), D_t - 1 = sum_e p_te (f_qe - 1).
 //
 // Two forms.  A batch whose scores a few SMs can stream takes one launch of one cluster of CTAs, which
 // count their own tokens, add the counts up through distributed shared memory and go on to the pass.
@@ -102,7 +104,7 @@ __device__ __forceinline__ void bal_count(const BalanceParams& p, int lo, int hi
   }
 }
 
-// The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe.  LANES lanes share a row (a warp
+// The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe - 1.  LANES lanes share a row (a warp
 // takes 32 / LANES rows side by side) and R such sets of rows are in flight; lane l of a row holds experts
 // VEC (l + LANES j) .. + VEC - 1.  Returns the lane's sum of D (lane 0 of each row's); nan: some score
 // was a NaN or infinite.
@@ -162,7 +164,7 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
       dot[r] *= inv;
       g[r] = wq * inv;
       if (t0 + r * kSide < hi) {
-        if (lane == 0) acc += dot[r];
+        if (lane == 0 && sum[r] != 0.f) acc += 1.f + dot[r];
         nan |= !(fabsf(sum[r]) <= 3.4028234e38f);
       }
     }
@@ -207,9 +209,10 @@ __device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs
     const int b = sq.begin(q), e = sq.begin(q + 1);
     if (b >= t1) break;
     if (max(b, t0) >= min(e, t1)) continue;
-    const float n = (float)(e - b), fs = (float)p.E / ((float)p.k * n), wq = p.coef / ((float)sq.filled * n);
+    const long long kn = (long long)p.k * (e - b);
+    const float per = 1.f / (float)kn, wq = p.coef / ((float)sq.filled * (float)(e - b));
     __syncthreads();  // the sequence before is done with f
-    for (int i = threadIdx.x; i < p.E; i += kBalThreads) f[i] = (float)p.counts[(long long)q * p.E + i] * fs;
+    for (int i = threadIdx.x; i < p.E; i += kBalThreads) f[i] = (float)((long long)p.counts[(long long)q * p.E + i] * p.E - kn) * per;
     __syncthreads();
     acc += (double)wq * bal_rows<NJ, VEC, R, LANES>(p, max(b, t0), min(e, t1), f, wq, nan);
   }

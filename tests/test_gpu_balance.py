@@ -100,6 +100,31 @@ def test_gradient_against_differences_of_the_loss():
     assert abs(num - ana) <= 128 * U * (scale * np.abs(d)).sum() + 1e-8
 
 
+def test_scores_past_32_bit_offsets():
+    """More than 2^31 scores, in a few long sequences and a short last one, which comes out as it does alone."""
+    T, E, k = 2_150_000, 1024, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    s = torch.rand((T, E), generator=g, device="cuda")
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    cu = [0, 1_000_000, T - 300, T]
+    out = lq.balance_loss(s, idx, 0.3, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    alone = lq.balance_loss(s[-300:], idx[-300:], 0.1)  # a third of the weight: three sequences share it
+    assert torch.equal(out["counts"][2], alone["counts"][0]) and int(out["counts"].sum()) == T * k
+    d, ref = out["dscores"][-300:], alone["dscores"]
+    assert (d - ref).abs().max() <= 16 * U * ref.abs().max()
+    assert abs(float(out["loss"]) - 0.3) < 1e-2  # uniform choices: balanced but for chance
+    del s, idx, out, d
+    torch.cuda.empty_cache()
+
+
+def test_every_expert_chosen_is_balance():
+    """k = E: f is 1 everywhere, so the loss is its weight and the gradient exactly zero."""
+    T, E = 500, 8
+    s, idx = inputs(T, E, E, 31)
+    out = lq.balance_loss(s.cuda(), idx.cuda(), 0.3)
+    assert not out["dscores"].any() and abs(float(out["loss"]) - 0.3) <= 8 * U * 0.3
+
+
 def test_slots_without_an_expert_zero_rows_and_equal_experts():
     T, E, k = 40, 64, 4
     s, idx = inputs(T, E, k, 5)

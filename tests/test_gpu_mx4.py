@@ -344,6 +344,26 @@ def test_streams_and_graph_replay():
     assert torch.equal(y, lq.mx4_gemm(lq.mx4_quant(a[3], offsets=o), b))
 
 
+def test_matrices_past_32_bit_offsets():
+    """More than 2^31 elements in the rows and in the result: the last rows come out as they do alone."""
+    M, K, N = 270000, 8192, 8192
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, M, 30000):
+        x[i:i + 30000].normal_(generator=g)
+    w = lq.mx4_quant(torch.randn((N, K), generator=g, device="cuda", dtype=torch.bfloat16))
+    q, last = lq.mx4_quant(x), lq.mx4_quant(x[-200:])
+    c = lq.mx4_gemm(q, w)
+    # the small product sums K in parts (too few tiles): fp32 sums in another order, rounded to bf16
+    a, b = c[-200:].float(), lq.mx4_gemm(last, w).float()
+    assert (a - b).abs().max() <= 2.0 ** -7 * b.abs().max()
+    del c
+    v = lq.mx4_dequant(q)
+    assert torch.equal(v[-200:], lq.mx4_dequant(last)) and torch.equal(v[:200], lq.mx4_dequant(lq.mx4_quant(x[:200])))
+    del x, q, v
+    torch.cuda.empty_cache()
+
+
 def test_two_graphs_at_once_and_alternating():
     """Two captured graphs of the operators, replayed on two streams at the same time and in turn: they share
     no workspace."""
