@@ -118,11 +118,11 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 }
 constexpr int kMx4PartPitch = 132;  // floats from row to row of a split tile's parts
 
-// Writes 16 bytes of a row of c, those columns before `cols` only.
+// Writes 16 bytes of a row of c (on a 16-byte boundary), those columns before `cols` only.
 template <typename T>
-__device__ __forceinline__ void mx4_store16(T* dst, int c0, int cols, bool vec, const uint4& v) {
+__device__ __forceinline__ void mx4_store16(T* dst, int c0, int cols, const uint4& v) {
   constexpr int kPer = 16 / sizeof(T);
-  if (vec && c0 + kPer <= cols) {
+  if (c0 + kPer <= cols) {
     *reinterpret_cast<uint4*>(dst) = v;
     return;
   }
@@ -136,15 +136,37 @@ __device__ __forceinline__ void mx4_store16(T* dst, int c0, int cols, bool vec, 
         dst[j] = __ushort_as_bfloat16((unsigned short)(vw[j >> 1] >> (16 * (j & 1))));
     }
 }
+// Writes a row of c on any boundary, one word a lane (lane l of LANES: word l), those columns before
+// `cols` (counted from the row's start here) only.  bf16 rows that begin between two words are written
+// a column later: each lane its upper value and the next lane's lower, the first and last column apart.
+template <int LANES, typename T>
+__device__ __forceinline__ void mx4_store_words(T* row, uint32_t w, int cols, bool live, int l) {
+  if constexpr (sizeof(T) == 4) {
+    if (live && l < cols) row[l] = __uint_as_float(w);
+  } else {
+    const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1, LANES);
+    if (!live) return;
+    uint16_t* h = reinterpret_cast<uint16_t*>(row);
+    if (((uintptr_t)row & 3) == 0) {
+      if (2 * l + 1 < cols) *reinterpret_cast<uint32_t*>(h + 2 * l) = w;
+      else if (2 * l < cols) h[2 * l] = (uint16_t)w;
+    } else {
+      if (l == 0 && cols > 0) h[0] = (uint16_t)w;
+      if (l + 1 < LANES && 2 * l + 2 < cols) *reinterpret_cast<uint32_t*>(h + 2 * l + 1) = (w >> 16) | (next << 16);
+      else if (2 * l + 1 < cols) h[2 * l + 1] = (uint16_t)(w >> 16);
+    }
+  }
+}
 // Rows a staging round holds: the box's 2 KB in rows of kWords words.
 __host__ __device__ constexpr int mx4_round_rows(int words) { return 2048 / (4 * words); }
 
 // Writes kWords words (64 or 128 bytes) of each of a warp's 32 rows of c, rows from `row`: lane l holds
 // row row + l's.  They go through the warp's 2 KB staging box (32 rows of 64 bytes, or twice 16 rows of
 // 128; 16-byte chunks swizzled as the tensor map of c says), which a TMA store then writes while the
-// warp goes on; a round with rows past `valid` (they may be another group's) or columns past p.c_cols, or a
-// c whose rows are not 16-byte aligned, is written by the lanes instead, neighbouring ones a row's neighbouring chunks.
-// col: first column; columns past p.c_cols are not written.
+// warp goes on.  A round with rows past `valid` (they may be another group's) or columns past p.c_cols is
+// written by the lanes instead, 16 bytes each, and one of a c whose rows are not 16-byte aligned a word
+// each (16384 x 1024 x 2048 into bf16 rows 1024 apart 20 us, 1028 apart 39, 1025 apart 43).  col: first
+// column; columns past p.c_cols are not written.
 template <int kWords, typename T>
 __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* box, const uint32_t (&w)[kWords],
                                                int row, int col, int valid, int lane) {
@@ -176,13 +198,25 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* 
     }
     __syncwarp();
     T* c = static_cast<T*>(p.c) + (long long)(row + g * kRows) * p.ldc;
+    if (!p.vec) {
+      constexpr int kSide = 32 / kWords;  // rows side by side
+      const int l = lane % kWords;
+#pragma unroll 4
+      for (int i = 0; i < kRows / kSide; ++i) {
+        const int rr = i * kSide + lane / kWords;
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(
+            box + rr * 4 * kWords + (((l >> 2) ^ ((rr >> kShift) & (kChunks - 1))) << 4) + (l & 3) * 4);
+        mx4_store_words<kWords>(c + (long long)rr * p.ldc + col, v, p.c_cols - col, g * kRows + rr < valid, l);
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < kRows * kChunks / 32; ++i) {
       const int rr = i * (32 / kChunks) + lane / kChunks;
       if (g * kRows + rr >= valid || c0 >= p.c_cols) continue;
       const uint4 v =
           *reinterpret_cast<const uint4*>(box + rr * 4 * kWords + ((q ^ ((rr >> kShift) & (kChunks - 1))) << 4));
-      mx4_store16(c + (long long)rr * p.ldc + c0, c0, p.c_cols, p.vec, v);
+      mx4_store16(c + (long long)rr * p.ldc + c0, c0, p.c_cols, v);
     }
   }
 }
@@ -271,6 +305,8 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
       if (lane == 0) {
         const int brow0 = g * p.N + nt * BN;
         const int sb0 = g * p.b_tiles + nt * (BN / 128);
+        // a tile of few rows loads 4 KB of A a k-block, not 16 (one token's 16 experts 7.6 us against 9.0,
+        // 32 x 8192 x 7168 10.1 against 12.6)
         const bool few = valid <= 32;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort, p.status)) {

@@ -357,7 +357,8 @@ int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_
   p.partial = reinterpret_cast<double*>(static_cast<char*>(scratch) + 256);
   p.status = status;
   const bool vec = E % 4 == 0 && (((uintptr_t)scores | (uintptr_t)dscores) & 15) == 0;
-  // sets of rows in flight: what fits 64 registers
+  // sets of rows in flight: what fits 64 registers; rows of few experts share a warp (262144 x 8 19 us
+  // against 39 with a row a warp, 65536 x 64 15 against 19)
   if (vec) {
     if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st);
     if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st);

@@ -198,10 +198,12 @@ def test_dense_product(M, N, K, out):
     check_product(np64(c), ref, mag, K, out)
 
 
-@pytest.mark.parametrize("out,pitch", [(torch.bfloat16, 136), (torch.bfloat16, 131), (torch.float32, 132),
-                                       (torch.float32, 131)])
-def test_product_into_strided_output_leaves_the_rest(out, pitch):
-    M, N, K = 140, 130, 320
+@pytest.mark.parametrize("out,pitch,N", [(torch.bfloat16, 136, 130), (torch.bfloat16, 131, 130), (torch.float32, 132, 130),
+                                         (torch.float32, 131, 130), (torch.bfloat16, 131, 1), (torch.bfloat16, 131, 65),
+                                         (torch.bfloat16, 133, 64), (torch.bfloat16, 133, 127), (torch.float32, 67, 65),
+                                         (torch.bfloat16, 2051, 2050), (torch.float32, 2051, 2051)])
+def test_product_into_strided_output_leaves_the_rest(out, pitch, N):
+    M, K = 140 if N < 2000 else 2100, 320
     a, b = rows((M, K), 1), rows((N, K), 2)
     buf = torch.full((M + 2, pitch), 7.0, dtype=out, device="cuda")
     lq.mx4_gemm(lq.mx4_quant(a.cuda()), lq.mx4_quant(b.cuda()), out=buf[1:M + 1, :N])
@@ -243,6 +245,17 @@ def check_swiglu(got, c, mag, K):
     tol = (2.0 ** -8 + 2.0 ** -15) * np.abs(ref) + 1.1 * eg * (np.abs(u) + eu) + (s + 1.1 * eg) * eu + 1e-30
     err = np.abs(got - ref)
     assert (err <= tol).all(), float((err - tol).max())
+
+
+@pytest.mark.parametrize("pitch", [128, 129, 136])
+def test_swiglu_into_strided_output_leaves_the_rest(pitch):
+    M, h, K = 300, 128, 320
+    a, w1, w3 = rows((M, K), 3), rows((h, K), 4, spread=0) / K ** 0.5, rows((h, K), 5, spread=0)
+    buf = torch.full((M + 2, pitch), 7.0, dtype=torch.bfloat16, device="cuda")
+    lq.mx4_gemm(lq.mx4_quant(a.cuda()), lq.mx4_quant_w13(w1.cuda(), w3.cuda()), swiglu=True, out=buf[1:M + 1, :h])
+    b = np.stack([mx.values(np64(w1)).reshape(-1, 64, K), mx.values(np64(w3)).reshape(-1, 64, K)], 1).reshape(2 * h, K)
+    check_swiglu(np64(buf[1:M + 1, :h]), *mx.product(mx.values(np64(a)), b), K)
+    assert (buf[0] == 7).all() and (buf[M + 1] == 7).all() and (buf[:, h:] == 7).all()
 
 
 @pytest.mark.parametrize("M,h,K", [(1, 64, 32), (5, 192, 288), (129, 128, 512), (300, 512, 2048), (1030, 320, 256),
