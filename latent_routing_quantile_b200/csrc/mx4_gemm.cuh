@@ -136,25 +136,39 @@ __device__ __forceinline__ void mx4_store16(T* dst, int c0, int cols, const uint
         dst[j] = __ushort_as_bfloat16((unsigned short)(vw[j >> 1] >> (16 * (j & 1))));
     }
 }
-// Writes a row of c on any boundary, one word a lane (lane l of LANES: word l), those columns before
-// `cols` (counted from the row's start here) only.  bf16 rows that begin between two words are written
-// a column later: each lane its upper value and the next lane's lower, the first and last column apart.
-template <int LANES, typename T>
-__device__ __forceinline__ void mx4_store_words(T* row, uint32_t w, int cols, bool live, int l) {
-  if constexpr (sizeof(T) == 4) {
-    if (live && l < cols) row[l] = __uint_as_float(w);
-  } else {
-    const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1, LANES);
-    if (!live) return;
-    uint16_t* h = reinterpret_cast<uint16_t*>(row);
-    if (((uintptr_t)row & 3) == 0) {
-      if (2 * l + 1 < cols) *reinterpret_cast<uint32_t*>(h + 2 * l) = w;
-      else if (2 * l < cols) h[2 * l] = (uint16_t)w;
-    } else {
-      if (l == 0 && cols > 0) h[0] = (uint16_t)w;
-      if (l + 1 < LANES && 2 * l + 2 < cols) *reinterpret_cast<uint32_t*>(h + 2 * l + 1) = (w >> 16) | (next << 16);
-      else if (2 * l + 1 < cols) h[2 * l + 1] = (uint16_t)(w >> 16);
+// Writes the first `bytes` bytes of row rr of a staging box to `row`, on any boundary; lane q of the row's
+// kChunks.  The 16-byte chunks of memory that lie inside are written whole, each put together from two
+// chunks of the box, and the values before the first and behind the last one by one.
+template <int kChunks, typename T>
+__device__ __forceinline__ void mx4_store_row(const uint8_t* box, int rr, int swizzle, T* row, int bytes, int q) {
+  const uint8_t* src = box + rr * 16 * kChunks;
+  auto chunk = [&](int j) { return src + ((j ^ swizzle) << 4); };
+  const int s = (int)(-(uintptr_t)row & 15);               // bytes before the first whole chunk of memory
+  const int whole = bytes > s ? (bytes - s) >> 4 : 0;
+  if (q < whole) {
+    uint4 a = *reinterpret_cast<const uint4*>(chunk(q));
+    if (s) {  // bytes [s, s + 16) of chunks q and q + 1
+      const uint4 n = *reinterpret_cast<const uint4*>(chunk(q + 1));
+      uint32_t w[6] = {a.x, a.y, a.z, a.w, n.x, n.y}, z[2] = {n.z, n.w};
+      if (s & 8) {
+        w[0] = w[2]; w[1] = w[3]; w[2] = w[4]; w[3] = w[5]; w[4] = z[0]; w[5] = z[1];
+      }
+      if (s & 4) {
+        w[0] = w[1]; w[1] = w[2]; w[2] = w[3]; w[3] = w[4]; w[4] = w[5];
+      }
+      if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+      }
+      a = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(row) + s + 16 * q) = a;
+  }
+  const int head = min(s, bytes) / (int)sizeof(T), behind = whole ? s + 16 * whole : min(s, bytes);
+  const int edges = head + (bytes - behind) / (int)sizeof(T);
+  for (int j = q; j < edges; j += kChunks) {
+    const int e = j < head ? j : behind / (int)sizeof(T) + j - head, at = e * (int)sizeof(T);
+    row[e] = *reinterpret_cast<const T*>(chunk(at >> 4) + (at & 15));
   }
 }
 // Rows a staging round holds: the box's 2 KB in rows of kWords words.
@@ -163,10 +177,10 @@ __host__ __device__ constexpr int mx4_round_rows(int words) { return 2048 / (4 *
 // Writes kWords words (64 or 128 bytes) of each of a warp's 32 rows of c, rows from `row`: lane l holds
 // row row + l's.  They go through the warp's 2 KB staging box (32 rows of 64 bytes, or twice 16 rows of
 // 128; 16-byte chunks swizzled as the tensor map of c says), which a TMA store then writes while the
-// warp goes on.  A round with rows past `valid` (they may be another group's) or columns past p.c_cols is
-// written by the lanes instead, 16 bytes each, and one of a c whose rows are not 16-byte aligned a word
-// each (16384 x 1024 x 2048 into bf16 rows 1024 apart 20 us, 1028 apart 39, 1025 apart 43).  col: first
-// column; columns past p.c_cols are not written.
+// warp goes on.  A round with rows past `valid` (they may be another group's) or columns past p.c_cols, or
+// of a c whose rows are not 16-byte aligned, is written by the lanes instead (13620 x 6080 x 1536 into bf16
+// 66 us, 6076 or 6077 wide 140; into fp32 89 and, 6078 wide, 163; 264 with the bf16 rows' way, which is
+// bound by its instructions).  col: first column; columns past p.c_cols are not written.
 template <int kWords, typename T>
 __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* box, const uint32_t (&w)[kWords],
                                                int row, int col, int valid, int lane) {
@@ -198,25 +212,30 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* 
     }
     __syncwarp();
     T* c = static_cast<T*>(p.c) + (long long)(row + g * kRows) * p.ldc;
-    if (!p.vec) {
-      constexpr int kSide = 32 / kWords;  // rows side by side
-      const int l = lane % kWords;
-#pragma unroll 4
-      for (int i = 0; i < kRows / kSide; ++i) {
-        const int rr = i * kSide + lane / kWords;
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(
-            box + rr * 4 * kWords + (((l >> 2) ^ ((rr >> kShift) & (kChunks - 1))) << 4) + (l & 3) * 4);
-        mx4_store_words<kWords>(c + (long long)rr * p.ldc + col, v, p.c_cols - col, g * kRows + rr < valid, l);
-      }
-      continue;
-    }
+    if (p.vec) {  // 16 bytes a lane
 #pragma unroll
-    for (int i = 0; i < kRows * kChunks / 32; ++i) {
-      const int rr = i * (32 / kChunks) + lane / kChunks;
-      if (g * kRows + rr >= valid || c0 >= p.c_cols) continue;
-      const uint4 v =
-          *reinterpret_cast<const uint4*>(box + rr * 4 * kWords + ((q ^ ((rr >> kShift) & (kChunks - 1))) << 4));
-      mx4_store16(c + (long long)rr * p.ldc + c0, c0, p.c_cols, v);
+      for (int i = 0; i < kRows * kChunks / 32; ++i) {
+        const int rr = i * (32 / kChunks) + lane / kChunks;
+        if (g * kRows + rr >= valid || c0 >= p.c_cols) continue;
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(box + rr * 4 * kWords + ((q ^ ((rr >> kShift) & (kChunks - 1))) << 4));
+        mx4_store16(c + (long long)rr * p.ldc + c0, c0, p.c_cols, v);
+      }
+    } else if constexpr (sizeof(T) == 4) {  // rows on 4-byte boundaries: a warp a row, a word a lane
+#pragma unroll
+      for (int rr = 0; rr < kRows; ++rr) {
+        const float v = *reinterpret_cast<const float*>(
+            box + rr * 4 * kWords + (((lane >> 2) ^ ((rr >> kShift) & (kChunks - 1))) << 4) + (lane & 3) * 4);
+        if (g * kRows + rr < valid && col + lane < p.c_cols) c[(long long)rr * p.ldc + col + lane] = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRows * kChunks / 32; ++i) {
+        const int rr = i * (32 / kChunks) + lane / kChunks;
+        if (g * kRows + rr < valid && col < p.c_cols)
+          mx4_store_row<kChunks>(box, rr, (rr >> kShift) & (kChunks - 1), c + (long long)rr * p.ldc + col,
+                                 min(4 * kWords, (p.c_cols - col) * (int)sizeof(T)), q);
+      }
     }
   }
 }
