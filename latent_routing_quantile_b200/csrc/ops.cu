@@ -123,7 +123,9 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
   const bool fits = (long long)p.S * p.E <= kBalHistInts;  // the cluster form's shared counters
   if (fits && (long long)p.T * p.E <= (1ll << 19)) {
     int ctas = 1;
-    while (ctas < kBalMaxCluster && ctas * kRound < p.T) ctas *= 2;  // one round of rows each
+    // CTAs: a round of rows each, and at most some two sequences each, which a CTA takes in turn (a few
+    // microseconds each)
+    while (ctas < kBalMaxCluster && (ctas * kRound < p.T || 2 * ctas < std::min(p.S, p.T))) ctas *= 2;
     p.chunk = (p.T + ctas - 1) / ctas;
     static unsigned done = 0;
     auto kern = balance_cluster_kernel<NJ, VEC, R, LANES>;
@@ -132,12 +134,14 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
     return LMOE_OK;
   }
   CK(cudaMemsetAsync(p.counts, 0, (size_t)p.S * p.E * sizeof(int32_t), st));
-  // counting: runs of at least 64 tokens, a block an SM
-  p.chunk = std::max(64, (p.T + sms - 1) / sms);
+  // counting: runs of some 64 tokens, fewer where the sequences are shorter (a block takes its sequences in
+  // turn), at most a block an SM
+  const int per_seq = (p.T + p.S - 1) / p.S;
+  p.chunk = std::max(std::min(64, per_seq), (p.T + sms - 1) / sms);
   CK(launch_k(balance_count_kernel, dim3((p.T + p.chunk - 1) / p.chunk), dim3(kBalThreads), 0, st, 1, p));
-  // the pass: at least one round of rows a block, at most the two blocks an SM that its registers allow
+  // the pass: one round of rows a block, or a sequence, at most the two blocks an SM that its registers allow
   const int blocks = std::min(2 * sms, kBalMaxBlocks);
-  p.chunk = std::max(kRound, (p.T + blocks - 1) / blocks);
+  p.chunk = std::max(std::min(kRound, per_seq), (p.T + blocks - 1) / blocks);
   CK(launch_k(balance_kernel<NJ, VEC, R, LANES>, dim3((p.T + p.chunk - 1) / p.chunk), dim3(kBalThreads), 0, st, 1, p));
   return LMOE_OK;
 }
