@@ -38,7 +38,7 @@ struct Mx4GemmParams {
   CUtensorMap tmB;   // codes [groups N, K / 2] u8, box 128 bytes x the tile's width
   CUtensorMap tmSA;  // scale atoms, see make_map_atoms: one row tile a box
   CUtensorMap tmSB;  // one or two (256-wide tiles) row tiles a box
-  CUtensorMap tmC;   // c, boxes of a staging round (mx4_store_rows); used when vec
+  CUtensorMap tmC;   // c, boxes of a staging round (mx4_store_rows); used when align is 16
   Mx4Rows rows;      // A's groups
   int N;             // rows of each B matrix
   int b_tiles;       // row tiles of each B matrix: ceil(N / 128)
@@ -49,7 +49,7 @@ struct Mx4GemmParams {
   long long ldc;
   int c_cols;        // columns of c
   int zero_rest;     // 1: rows of c that belong to no group are set to zero
-  int vec;           // every row of c starts on a 16-byte boundary
+  int align;         // every row of c starts on a boundary of 16, 8, 4 or 2 bytes
   uint32_t* status;
 };
 
@@ -118,23 +118,46 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 }
 constexpr int kMx4PartPitch = 132;  // floats from row to row of a split tile's parts
 
-// Writes 16 bytes of a row of c (on a 16-byte boundary), those columns before `cols` only.
-template <typename T>
-__device__ __forceinline__ void mx4_store16(T* dst, int c0, int cols, const uint4& v) {
-  constexpr int kPer = 16 / sizeof(T);
-  if (c0 + kPer <= cols) {
-    *reinterpret_cast<uint4*>(dst) = v;
-    return;
-  }
-  const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+// Writes a staging round to rows of c on a boundary of UNIT words: a unit a lane, neighbouring lanes a row's
+// neighbouring units, rows before `valid` and columns before `cols` only.
+template <int UNIT, int kRows, int kChunks, int kShift, typename T>
+__device__ __forceinline__ void mx4_store_units(const uint8_t* box, T* c, long long ldc, int col, int cols, int valid,
+                                                int lane) {
+  constexpr int kLanes = 4 * kChunks / UNIT;         // lanes a row
+  constexpr int kPer = 4 * UNIT / (int)sizeof(T);    // columns a unit
+  const int l = lane % kLanes, cc = col + kPer * l, first = l * UNIT;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (c0 + j < cols) {
-      if constexpr (sizeof(T) == 4)
-        dst[j] = __uint_as_float(vw[j]);
-      else
-        dst[j] = __ushort_as_bfloat16((unsigned short)(vw[j >> 1] >> (16 * (j & 1))));
+  for (int i = 0; i < kRows * kLanes / 32; ++i) {
+    const int rr = i * (32 / kLanes) + lane / kLanes;
+    const int chunk = (first >> 2) ^ ((rr >> kShift) & (kChunks - 1));
+    const uint8_t* src = box + rr * 16 * kChunks + 16 * chunk + 4 * (first & 3);
+    uint32_t w[UNIT];
+    if constexpr (UNIT == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (UNIT == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(src);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(src);
     }
+    if (rr >= valid || cc >= cols) continue;
+    T* dst = c + (long long)rr * ldc + cc;
+    if (cc + kPer <= cols) {
+      if constexpr (UNIT == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (UNIT == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (cc + j < cols) {
+          if constexpr (sizeof(T) == 4)
+            dst[j] = __uint_as_float(w[j]);
+          else
+            dst[j] = __ushort_as_bfloat16((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
+        }
+    }
+  }
 }
 // Writes the first `bytes` bytes of row rr of a staging box to `row`, on any boundary; lane q of the row's
 // kChunks.  The 16-byte chunks of memory that lie inside are written whole, each put together from two
@@ -178,9 +201,12 @@ __host__ __device__ constexpr int mx4_round_rows(int words) { return 2048 / (4 *
 // row row + l's.  They go through the warp's 2 KB staging box (32 rows of 64 bytes, or twice 16 rows of
 // 128; 16-byte chunks swizzled as the tensor map of c says), which a TMA store then writes while the
 // warp goes on.  A round with rows past `valid` (they may be another group's) or columns past p.c_cols, or
-// of a c whose rows are not 16-byte aligned, is written by the lanes instead (13620 x 6080 x 1536 into bf16
-// 66 us, 6076 or 6077 wide 140; into fp32 89 and, 6078 wide, 163; 264 with the bf16 rows' way, which is
-// bound by its instructions).  col: first column; columns past p.c_cols are not written.
+// of a c whose rows are not 16-byte aligned, is written by the lanes instead: in units of 8 or 4 bytes if
+// every row starts on such a boundary, else each row in the 16-byte chunks that lie in it.  13620 x N x
+// 1536 in us, aligned rows first, in units and (in chunks): into bf16 rows 6080 wide 65, 6076 (8 bytes) 77
+// (143), 6078 (4) 115 (144), 6077 (2) (145); into fp32 rows 89, 6078 (8) 127 (172), 6077 (4) 141 (164).  A
+// SwiGLU's rounds (16 words) have no units: their code in that kernel spilled registers and took its
+// smallest grouped products from 53 to 63 us.  col: first column; columns past p.c_cols are not written.
 template <int kWords, typename T>
 __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* box, const uint32_t (&w)[kWords],
                                                int row, int col, int valid, int lane) {
@@ -188,7 +214,6 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* 
   constexpr int kChunks = kWords / 4;            // chunks a row: 4 or 8
   constexpr int kRows = mx4_round_rows(kWords);  // 32 or 16
   constexpr int kShift = kChunks == 4 ? 1 : 0;   // two rows of 64 bytes share a 128-byte line of the box
-  const int q = lane % kChunks, c0 = col + q * kPer;
 #pragma unroll
   for (int g = 0; g < 32 / kRows; ++g) {
     if (g * kRows >= valid) break;
@@ -201,7 +226,7 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* 
         *reinterpret_cast<uint4*>(box + rr * 4 * kWords + ((j ^ ((rr >> kShift) & (kChunks - 1))) << 4)) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
-    if (p.vec && (g + 1) * kRows <= valid && col + kChunks * kPer <= p.c_cols) {
+    if (p.align == 16 && (g + 1) * kRows <= valid && col + kChunks * kPer <= p.c_cols) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -212,29 +237,19 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* 
     }
     __syncwarp();
     T* c = static_cast<T*>(p.c) + (long long)(row + g * kRows) * p.ldc;
-    if (p.vec) {  // 16 bytes a lane
-#pragma unroll
-      for (int i = 0; i < kRows * kChunks / 32; ++i) {
-        const int rr = i * (32 / kChunks) + lane / kChunks;
-        if (g * kRows + rr >= valid || c0 >= p.c_cols) continue;
-        const uint4 v =
-            *reinterpret_cast<const uint4*>(box + rr * 4 * kWords + ((q ^ ((rr >> kShift) & (kChunks - 1))) << 4));
-        mx4_store16(c + (long long)rr * p.ldc + c0, c0, p.c_cols, v);
-      }
-    } else if constexpr (sizeof(T) == 4) {  // rows on 4-byte boundaries: a warp a row, a word a lane
-#pragma unroll
-      for (int rr = 0; rr < kRows; ++rr) {
-        const float v = *reinterpret_cast<const float*>(
-            box + rr * 4 * kWords + (((lane >> 2) ^ ((rr >> kShift) & (kChunks - 1))) << 4) + (lane & 3) * 4);
-        if (g * kRows + rr < valid && col + lane < p.c_cols) c[(long long)rr * p.ldc + col + lane] = v;
-      }
+    if (p.align == 16) {
+      mx4_store_units<4, kRows, kChunks, kShift>(box, c, p.ldc, col, p.c_cols, valid - g * kRows, lane);
+    } else if (kWords == 32 && p.align == 8) {
+      mx4_store_units<2, kRows, kChunks, kShift>(box, c, p.ldc, col, p.c_cols, valid - g * kRows, lane);
+    } else if (kWords == 32 && p.align == 4) {
+      mx4_store_units<1, kRows, kChunks, kShift>(box, c, p.ldc, col, p.c_cols, valid - g * kRows, lane);
     } else {
 #pragma unroll
       for (int i = 0; i < kRows * kChunks / 32; ++i) {
         const int rr = i * (32 / kChunks) + lane / kChunks;
         if (g * kRows + rr < valid && col < p.c_cols)
           mx4_store_row<kChunks>(box, rr, (rr >> kShift) & (kChunks - 1), c + (long long)rr * p.ldc + col,
-                                 min(4 * kWords, (p.c_cols - col) * (int)sizeof(T)), q);
+                                 min(4 * kWords, (p.c_cols - col) * (int)sizeof(T)), lane % kChunks);
       }
     }
   }

@@ -306,9 +306,10 @@ int lmoe_mx4_gemm(const uint8_t* a_elems, const uint8_t* a_scales, const uint8_t
   p.ldc = ldc;
   p.c_cols = cols;
   p.zero_rest = (flags & LMOE_MX4_ZERO_REST) ? 1 : 0;
-  p.vec = row_access(c, ldc, c_dtype) != MX4_ELEMENTS;
+  p.align = 16;
+  while (((uint64_t)(uintptr_t)c | (uint64_t)ldc * (c_dtype == LMOE_F32 ? 4 : 2)) & (p.align - 1)) p.align /= 2;
   p.status = status;
-  if (p.vec && !make_map_c(&p.tmC, c, M, cols, ldc, c_dtype == LMOE_F32, swiglu ? 16 : 32)) return LMOE_ECUDA;
+  if (p.align == 16 && !make_map_c(&p.tmC, c, M, cols, ldc, c_dtype == LMOE_F32, swiglu ? 16 : 32)) return LMOE_ECUDA;
   cudaStream_t st = (cudaStream_t)stream;
   auto launch = [&](auto type, auto glu) -> int {
     using T = decltype(type);

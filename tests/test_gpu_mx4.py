@@ -201,7 +201,9 @@ def test_dense_product(M, N, K, out):
 @pytest.mark.parametrize("out,pitch,N", [(torch.bfloat16, 136, 130), (torch.bfloat16, 131, 130), (torch.float32, 132, 130),
                                          (torch.float32, 131, 130), (torch.bfloat16, 131, 1), (torch.bfloat16, 131, 65),
                                          (torch.bfloat16, 133, 64), (torch.bfloat16, 133, 127), (torch.float32, 67, 65),
-                                         (torch.bfloat16, 2051, 2050), (torch.float32, 2051, 2051)])
+                                         (torch.bfloat16, 2051, 2050), (torch.float32, 2051, 2051), (torch.float32, 2050, 2049),
+                                         (torch.bfloat16, 132, 130), (torch.bfloat16, 132, 129), (torch.bfloat16, 132, 131),
+                                         (torch.float32, 134, 130), (torch.float32, 134, 129)])
 def test_product_into_strided_output_leaves_the_rest(out, pitch, N):
     M, K = 140 if N < 2000 else 2100, 320
     a, b = rows((M, K), 1), rows((N, K), 2)
@@ -247,7 +249,7 @@ def check_swiglu(got, c, mag, K):
     assert (err <= tol).all(), float((err - tol).max())
 
 
-@pytest.mark.parametrize("pitch", [128, 129, 136])
+@pytest.mark.parametrize("pitch", [128, 129, 130, 132, 136])
 def test_swiglu_into_strided_output_leaves_the_rest(pitch):
     M, h, K = 300, 128, 320
     a, w1, w3 = rows((M, K), 3), rows((h, K), 4, spread=0) / K ** 0.5, rows((h, K), 5, spread=0)
