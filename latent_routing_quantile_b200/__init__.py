@@ -496,7 +496,7 @@ def _status_word(index: int) -> int:
             raise LmoeError("the first operator call on a device cannot be captured: make one before the capture")
         word = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
         torch.cuda.synchronize(index)
-        w = _status_words[index] = (word, word.data_ptr())
+        w = _status_words.setdefault(index, (word, word.data_ptr()))  # of two threads' words the first stays
     return w[1]
 
 

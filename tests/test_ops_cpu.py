@@ -200,3 +200,26 @@ def test_flag_constants_match_the_header():
     for name, v in (("MX4_SWIGLU", lq.MX4_SWIGLU), ("MX4_ZERO_REST", lq.MX4_ZERO_REST),
                     ("EXPERTS_MXFP4", lq.EXPERTS_MXFP4)):
         assert int(re.search(rf"#define LMOE_{name} (\d+)", text).group(1)) == v
+
+
+def test_first_calls_of_two_threads_share_one_status_word(monkeypatch):
+    """Both threads are past the look-up when the words are made: one word stays, and both get its address
+    (the other's memory goes back to the allocator, so no kernel may have been given it)."""
+    import threading
+    both, zeros, got = threading.Barrier(2, timeout=30), torch.zeros, []
+
+    def made_together(*shape, **kw):
+        word = zeros(*shape, dtype=kw["dtype"])
+        both.wait()
+        return word
+
+    monkeypatch.setattr(lq, "_status_words", {})
+    monkeypatch.setattr(lq.torch, "zeros", made_together)
+    monkeypatch.setattr(lq.torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(lq.torch.cuda, "synchronize", lambda index=None: None)
+    threads = [threading.Thread(target=lambda: got.append(lq._status_word(0))) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == [lq._status_words[0][1]] * 2
