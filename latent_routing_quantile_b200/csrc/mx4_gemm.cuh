@@ -118,80 +118,55 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 }
 constexpr int kMx4PartPitch = 132;  // floats from row to row of a split tile's parts
 
-// Writes a staging round to rows of c on a boundary of UNIT words: a unit a lane, neighbouring lanes a row's
-// neighbouring units, rows before `valid` and columns before `cols` only.
+// Writes a staging round to rows of c on a boundary of UNIT (4 or 2) words: a unit a lane, neighbouring
+// lanes a row's neighbouring units, rows before `valid` and columns before `cols` only.  c: the round's
+// first row and column.
 template <int UNIT, int kRows, int kChunks, int kShift, typename T>
-__device__ __forceinline__ void mx4_store_units(const uint8_t* box, T* c, long long ldc, int col, int cols, int valid,
-                                                int lane) {
+__device__ __forceinline__ void mx4_store_units(const uint8_t* box, T* c, long long ldc, int cols, int valid, int lane) {
+  using V = std::conditional_t<UNIT == 4, uint4, uint2>;
   constexpr int kLanes = 4 * kChunks / UNIT;         // lanes a row
   constexpr int kPer = 4 * UNIT / (int)sizeof(T);    // columns a unit
-  const int l = lane % kLanes, cc = col + kPer * l, first = l * UNIT;
-#pragma unroll
-  for (int i = 0; i < kRows * kLanes / 32; ++i) {
-    const int rr = i * (32 / kLanes) + lane / kLanes;
+  const int l = lane % kLanes, r0 = lane / kLanes, first = l * UNIT;
+  c += r0 * ldc + kPer * l;
+  const int left = cols - kPer * l;
+  auto unit = [&](int rr) {
     const int chunk = (first >> 2) ^ ((rr >> kShift) & (kChunks - 1));
-    const uint8_t* src = box + rr * 16 * kChunks + 16 * chunk + 4 * (first & 3);
-    uint32_t w[UNIT];
-    if constexpr (UNIT == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src);
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else if constexpr (UNIT == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(src);
-      w[0] = v.x; w[1] = v.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(src);
-    }
-    if (rr >= valid || cc >= cols) continue;
-    T* dst = c + (long long)rr * ldc + cc;
-    if (cc + kPer <= cols) {
-      if constexpr (UNIT == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-      else if constexpr (UNIT == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = w[0];
-    } else {
+    return box + rr * 16 * kChunks + 16 * chunk + 4 * (first & 3);
+  };
+  T* dst = c;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (cc + j < cols) {
-          if constexpr (sizeof(T) == 4)
-            dst[j] = __uint_as_float(w[j]);
-          else
-            dst[j] = __ushort_as_bfloat16((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
-        }
-    }
+  for (int i = 0; i < kRows * kLanes / 32; ++i, dst += 32 / kLanes * ldc) {
+    const int rr = i * (32 / kLanes) + r0;
+    const V v = *reinterpret_cast<const V*>(unit(rr));
+    if (rr < valid && left >= kPer) *reinterpret_cast<V*>(dst) = v;
+  }
+  if (left > 0 && left < kPer) {  // the unit that the last column lies in
+#pragma unroll 1
+    for (int rr = r0; rr < min(valid, kRows); rr += 32 / kLanes, c += 32 / kLanes * ldc)
+      for (int j = 0; j < left; ++j) c[j] = reinterpret_cast<const T*>(unit(rr))[j];
   }
 }
-// Writes the first `bytes` bytes of row rr of a staging box to `row`, on any boundary; lane q of the row's
-// kChunks.  The 16-byte chunks of memory that lie inside are written whole, each put together from two
-// chunks of the box, and the values before the first and behind the last one by one.
-template <int kChunks, typename T>
-__device__ __forceinline__ void mx4_store_row(const uint8_t* box, int rr, int swizzle, T* row, int bytes, int q) {
-  const uint8_t* src = box + rr * 16 * kChunks;
-  auto chunk = [&](int j) { return src + ((j ^ swizzle) << 4); };
-  const int s = (int)(-(uintptr_t)row & 15);               // bytes before the first whole chunk of memory
-  const int whole = bytes > s ? (bytes - s) >> 4 : 0;
-  if (q < whole) {
-    uint4 a = *reinterpret_cast<const uint4*>(chunk(q));
-    if (s) {  // bytes [s, s + 16) of chunks q and q + 1
-      const uint4 n = *reinterpret_cast<const uint4*>(chunk(q + 1));
-      uint32_t w[6] = {a.x, a.y, a.z, a.w, n.x, n.y}, z[2] = {n.z, n.w};
-      if (s & 8) {
-        w[0] = w[2]; w[1] = w[3]; w[2] = w[4]; w[3] = w[5]; w[4] = z[0]; w[5] = z[1];
-      }
-      if (s & 4) {
-        w[0] = w[1]; w[1] = w[2]; w[2] = w[3]; w[3] = w[4]; w[4] = w[5];
-      }
-      if (s & 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-      }
-      a = make_uint4(w[0], w[1], w[2], w[3]);
+// The same for rows on any boundary: a word a lane.  A bf16 row on an odd boundary takes the words that
+// lie in it, each put together from two of the box, and its first and last value by themselves.
+template <int kRows, int kChunks, typename T>
+__device__ __forceinline__ void mx4_store_words(const uint8_t* box, T* c, long long ldc, int cols, int valid, int lane) {
+  constexpr int kLanes = 4 * kChunks;  // lanes a row: 32, or 16 for two rows at once
+  const int l = lane % kLanes, r0 = lane / kLanes;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(box);
+  c += r0 * ldc;
+#pragma unroll 8  // 16: registers spill
+  for (int i = 0; i < 16; ++i, c += 32 / kLanes * ldc) {
+    const uint32_t w = words[32 * i + (lane ^ ((i & (kChunks - 1)) << 2))];
+    const bool row = i * (32 / kLanes) + r0 < valid;
+    if constexpr (sizeof(T) == 4) {
+      if (row && l < cols) c[l] = __uint_as_float(w);
+    } else {
+      const int odd = (int)((uintptr_t)c >> 1) & 1, e = 2 * l + odd, end = min(2 * kLanes, cols);
+      const uint32_t z = __funnelshift_r(w, __shfl_down_sync(0xffffffffu, w, 1), 16 * odd);
+      if (row && e + 1 < end) *reinterpret_cast<uint32_t*>(c + e) = z;
+      if (row && e + 1 == end) c[e] = __ushort_as_bfloat16((unsigned short)z);
+      if (row && odd && l == 0 && end > 0) c[0] = __ushort_as_bfloat16((unsigned short)w);
     }
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(row) + s + 16 * q) = a;
-  }
-  const int head = min(s, bytes) / (int)sizeof(T), behind = whole ? s + 16 * whole : min(s, bytes);
-  const int edges = head + (bytes - behind) / (int)sizeof(T);
-  for (int j = q; j < edges; j += kChunks) {
-    const int e = j < head ? j : behind / (int)sizeof(T) + j - head, at = e * (int)sizeof(T);
-    row[e] = *reinterpret_cast<const T*>(chunk(at >> 4) + (at & 15));
   }
 }
 // Rows a staging round holds: the box's 2 KB in rows of kWords words.
@@ -201,12 +176,13 @@ __host__ __device__ constexpr int mx4_round_rows(int words) { return 2048 / (4 *
 // row row + l's.  They go through the warp's 2 KB staging box (32 rows of 64 bytes, or twice 16 rows of
 // 128; 16-byte chunks swizzled as the tensor map of c says), which a TMA store then writes while the
 // warp goes on.  A round with rows past `valid` (they may be another group's) or columns past p.c_cols, or
-// of a c whose rows are not 16-byte aligned, is written by the lanes instead: in units of 8 or 4 bytes if
-// every row starts on such a boundary, else each row in the 16-byte chunks that lie in it.  13620 x N x
-// 1536 in us, aligned rows first, in units and (in chunks): into bf16 rows 6080 wide 65, 6076 (8 bytes) 77
-// (143), 6078 (4) 115 (144), 6077 (2) (145); into fp32 rows 89, 6078 (8) 127 (172), 6077 (4) 141 (164).  A
-// SwiGLU's rounds (16 words) have no units: their code in that kernel spilled registers and took its
-// smallest grouped products from 53 to 63 us.  col: first column; columns past p.c_cols are not written.
+// of a c whose rows are not 16-byte aligned, is written by the lanes instead: in units of 16 or 8 bytes if
+// every row starts on such a boundary, else in words.  13620 x N x 1536 in us: into bf16 rows 6080 wide 65,
+// 6076 (8 bytes) 71 (in words 104), 6078 (4) 104, 6077 (2) 107; into fp32 rows 86, 6078 (8) 105 (in words
+// 153), 6077 (4) 153.  What bounds those is each warp's instructions, so the loops have few.  A SwiGLU's
+// rounds (16 words) leave out the 8-byte units: with their code its kernel spills registers, and 135000
+// aligned rows of 384 values in 512 groups take 97 us for 71.  col: first column; columns past p.c_cols are
+// not written.
 template <int kWords, typename T>
 __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* box, const uint32_t (&w)[kWords],
                                                int row, int col, int valid, int lane) {
@@ -236,22 +212,13 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, uint8_t* 
       continue;
     }
     __syncwarp();
-    T* c = static_cast<T*>(p.c) + (long long)(row + g * kRows) * p.ldc;
-    if (p.align == 16) {
-      mx4_store_units<4, kRows, kChunks, kShift>(box, c, p.ldc, col, p.c_cols, valid - g * kRows, lane);
-    } else if (kWords == 32 && p.align == 8) {
-      mx4_store_units<2, kRows, kChunks, kShift>(box, c, p.ldc, col, p.c_cols, valid - g * kRows, lane);
-    } else if (kWords == 32 && p.align == 4) {
-      mx4_store_units<1, kRows, kChunks, kShift>(box, c, p.ldc, col, p.c_cols, valid - g * kRows, lane);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kRows * kChunks / 32; ++i) {
-        const int rr = i * (32 / kChunks) + lane / kChunks;
-        if (g * kRows + rr < valid && col < p.c_cols)
-          mx4_store_row<kChunks>(box, rr, (rr >> kShift) & (kChunks - 1), c + (long long)rr * p.ldc + col,
-                                 min(4 * kWords, (p.c_cols - col) * (int)sizeof(T)), lane % kChunks);
-      }
-    }
+    T* c = static_cast<T*>(p.c) + (long long)(row + g * kRows) * p.ldc + col;
+    if (p.align == 16)
+      mx4_store_units<4, kRows, kChunks, kShift>(box, c, p.ldc, p.c_cols - col, valid - g * kRows, lane);
+    else if (kWords == 32 && p.align == 8)
+      mx4_store_units<2, kRows, kChunks, kShift>(box, c, p.ldc, p.c_cols - col, valid - g * kRows, lane);
+    else
+      mx4_store_words<kRows, kChunks>(box, c, p.ldc, p.c_cols - col, valid - g * kRows, lane);
   }
 }
 
