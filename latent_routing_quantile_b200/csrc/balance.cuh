@@ -104,10 +104,53 @@ __device__ __forceinline__ void bal_count(const BalanceParams& p, int lo, int hi
   }
 }
 
+// Sums between these bounds have a reciprocal that every product here stays finite with; the rows of other
+// sums are left to bal_row_scaled.
+constexpr float kBalSumMin = 0x1p-60f, kBalSumMax = 0x1p60f;
+
+// One row by itself, LANES lanes a row (`there` is false for lanes without one): scores so small that 1 / R
+// overflows or so large that R does are scaled by a power of two first, which D does not see and the
+// gradient's 1 / R gives back.  A gradient past fp32 saturates at its largest value; a row of zeros has
+// no probabilities: it adds nothing and gets no gradient.  Returns D in the row's first lane.
+template <int LANES>
+__device__ __forceinline__ float bal_row_scaled(const float* srow, float* drow, int E, const float* f, float wq,
+                                                bool there, bool& nan) {
+  const int lane = threadIdx.x & (LANES - 1), end = there ? E : 0;
+  float top = 0.f;
+#pragma unroll 1
+  for (int e = lane; e < end; e += LANES) top = fmaxf(top, fabsf(srow[e]));
+#pragma unroll
+  for (int off = LANES / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float c = top < kBalSumMin ? 0x1p64f : (top > kBalSumMax ? 0x1p-64f : 1.f);
+  float sum = 0.f, dot = 0.f;
+#pragma unroll 1
+  for (int e = lane; e < end; e += LANES) {
+    const float v = srow[e] * c;
+    sum += v;
+    dot = fmaf(v, f[e], dot);
+  }
+#pragma unroll
+  for (int off = LANES / 2; off; off >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    dot += __shfl_xor_sync(0xffffffffu, dot, off);
+  }
+  nan |= !(fabsf(sum) <= 3.4028234e38f);
+  const bool some = sum != 0.f;
+  const float d = some ? dot / sum : 0.f;
+  if (drow) {
+#pragma unroll 1
+    for (int e = lane; e < end; e += LANES) {
+      const float g = some ? wq * (f[e] - d) / sum * c : 0.f;
+      drow[e] = isinf(g) ? copysignf(3.4028234e38f, g) : g;
+    }
+  }
+  return some && lane == 0 ? 1.f + d : 0.f;
+}
+
 // The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe - 1.  LANES lanes share a row (a warp
 // takes 32 / LANES rows side by side) and R such sets of rows are in flight; lane l of a row holds experts
 // VEC (l + LANES j) .. + VEC - 1.  Returns the lane's sum of D (lane 0 of each row's); nan: some score
-// was a NaN or infinite.
+// was a NaN or infinite (such a row's sum is one too, which leaves it to bal_row_scaled).
 template <int NJ, int VEC, int R, int LANES>
 __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
   constexpr int kSide = 32 / LANES;
@@ -157,16 +200,17 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
         dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], off);
       }
     float g[R];
+    unsigned skip = 0, rare = 0;  // sets in which this lane's row is not there or left to bal_row_scaled; in
+                                  // which some lane's is
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // a row of zeros has no probabilities: it adds nothing and gets no gradient
-      const float inv = sum[r] != 0.f ? 1.f / sum[r] : 0.f;
+      const bool there = t0 + r * kSide < hi, ok = sum[r] >= kBalSumMin && sum[r] <= kBalSumMax;
+      const float inv = 1.f / sum[r];
       dot[r] *= inv;
       g[r] = wq * inv;
-      if (t0 + r * kSide < hi) {
-        if (lane == 0 && sum[r] != 0.f) acc += 1.f + dot[r];
-        nan |= !(fabsf(sum[r]) <= 3.4028234e38f);
-      }
+      if (there && ok && lane == 0) acc += 1.f + dot[r];
+      if (!there || !ok) skip |= 1u << r;
+      if (__any_sync(0xffffffffu, there && !ok)) rare |= 1u << r;
     }
     if (p.dscores) {
 #pragma unroll
@@ -176,7 +220,7 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
         const float4 fv = fval(j);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          if (t0 + r * kSide >= hi) continue;
+          if ((skip >> r) & 1) continue;
           float* d = p.dscores + (long long)(t0 + r * kSide) * p.E + e;
           if constexpr (VEC == 4)
             *reinterpret_cast<float4*>(d) = make_float4(g[r] * (fv.x - dot[r]), g[r] * (fv.y - dot[r]),
@@ -185,6 +229,14 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
             *d = g[r] * (fv.x - dot[r]);
         }
       }
+    }
+#pragma unroll 1
+    for (int r = 0; rare >> r; ++r) {
+      if (!((rare >> r) & 1)) continue;
+      const int t = t0 + r * kSide;
+      const long long at = (long long)t * p.E;
+      acc += bal_row_scaled<LANES>(p.scores + at, p.dscores ? p.dscores + at : nullptr, p.E, f, wq,
+                                   t < hi && ((skip >> r) & 1), nan);
     }
   }
   return acc;
@@ -295,7 +347,7 @@ __device__ __forceinline__ double ld_cluster_double(const double* p, uint32_t ra
   return v;
 }
 template <int NJ, int VEC, int R, int LANES>
-__global__ void __launch_bounds__(kBalThreads) balance_cluster_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(kBalThreads, 1) balance_cluster_kernel(const BalanceParams p) {
   __shared__ int hist[kBalHistInts];
   __shared__ __align__(16) float f[1024];
   __shared__ double wsum[kBalThreads / 32], total;
