@@ -11,6 +11,8 @@
 // probabilities are never formed.  The pass is bound by memory (scores read, gradient written).
 // Near balance f and D are both close to 1 and f - D cancels, so both are held as what they differ from
 // 1 by, f from whole numbers: f_qe - 1 = (counts_qe E - k n_q) / (k n_q), D_t - 1 = sum_e p_te (f_qe - 1).
+// A token whose probabilities lie on experts that few chose has a D near 0, where D - 1 cancels in its
+// turn: rows of D < 1/2 are taken again with f and D themselves.
 //
 // Two forms.  A batch whose scores a few SMs can stream takes one launch of one cluster of CTAs, which
 // count their own tokens, add the counts up through distributed shared memory and go on to the pass.
@@ -26,6 +28,7 @@ constexpr int kBalThreads = 512;
 constexpr int kBalMaxBlocks = 1024;
 constexpr int kBalHistInts = 8192;   // shared counters of a block
 constexpr int kBalMaxCluster = 16;
+constexpr int kBalMaxE = 1024;
 
 struct BalanceParams {
   const float* scores;   // [T, E]
@@ -105,15 +108,16 @@ __device__ __forceinline__ void bal_count(const BalanceParams& p, int lo, int hi
 }
 
 // Sums between these bounds have a reciprocal that every product here stays finite with; the rows of other
-// sums are left to bal_row_scaled.
+// sums, and those of D < 1/2, are left to bal_row_alone.
 constexpr float kBalSumMin = 0x1p-60f, kBalSumMax = 0x1p60f;
 
-// One row by itself, LANES lanes a row (`there` is false for lanes without one): scores so small that 1 / R
-// overflows or so large that R does are scaled by a power of two first, which D does not see and the
-// gradient's 1 / R gives back.  A gradient past fp32 saturates at its largest value; a row of zeros has
-// no probabilities: it adds nothing and gets no gradient.  Returns D in the row's first lane.
+// One row by itself, LANES lanes a row (`there` is false for lanes without one).  f: shared, f - 1 and,
+// kBalMaxE further, f.  Scores so small that 1 / R overflows or so large that R does are scaled by a power
+// of two first, which D does not see and the gradient's 1 / R gives back.  D < 1/2 is summed as it is, D
+// above as D - 1.  A gradient past fp32 saturates at its largest value; a row of zeros has no
+// probabilities: it adds nothing and gets no gradient.  Returns D in the row's first lane.
 template <int LANES>
-__device__ __forceinline__ float bal_row_scaled(const float* srow, float* drow, int E, const float* f, float wq,
+__device__ __forceinline__ float bal_row_alone(const float* srow, float* drow, int E, const float* f, float wq,
                                                 bool there, bool& nan) {
   const int lane = threadIdx.x & (LANES - 1), end = there ? E : 0;
   float top = 0.f;
@@ -122,21 +126,24 @@ __device__ __forceinline__ float bal_row_scaled(const float* srow, float* drow, 
 #pragma unroll
   for (int off = LANES / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   const float c = top < kBalSumMin ? 0x1p64f : (top > kBalSumMax ? 0x1p-64f : 1.f);
-  float sum = 0.f, dot = 0.f;
+  float sum = 0.f, dot = 0.f, whole = 0.f;
 #pragma unroll 1
   for (int e = lane; e < end; e += LANES) {
     const float v = srow[e] * c;
     sum += v;
     dot = fmaf(v, f[e], dot);
+    whole = fmaf(v, f[kBalMaxE + e], whole);
   }
 #pragma unroll
   for (int off = LANES / 2; off; off >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, off);
     dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    whole += __shfl_xor_sync(0xffffffffu, whole, off);
   }
   nan |= !(fabsf(sum) <= 3.4028234e38f);
-  const bool some = sum != 0.f;
-  const float d = some ? dot / sum : 0.f;
+  const bool some = sum != 0.f, low = dot < -0.5f * sum;
+  const float d = some ? (low ? whole : dot) / sum : 0.f;
+  if (low) f += kBalMaxE;
   if (drow) {
 #pragma unroll 1
     for (int e = lane; e < end; e += LANES) {
@@ -144,13 +151,14 @@ __device__ __forceinline__ float bal_row_scaled(const float* srow, float* drow, 
       drow[e] = isinf(g) ? copysignf(3.4028234e38f, g) : g;
     }
   }
-  return some && lane == 0 ? 1.f + d : 0.f;
+  return some && lane == 0 ? (low ? d : 1.f + d) : 0.f;
 }
 
-// The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe - 1.  LANES lanes share a row (a warp
-// takes 32 / LANES rows side by side) and R such sets of rows are in flight; lane l of a row holds experts
-// VEC (l + LANES j) .. + VEC - 1.  Returns the lane's sum of D (lane 0 of each row's); nan: some score
-// was a NaN or infinite (such a row's sum is one too, which leaves it to bal_row_scaled).
+// The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe - 1 and, kBalMaxE further, f_qe.
+// LANES lanes share a row (a warp takes 32 / LANES rows side by side) and R such sets of rows are in flight;
+// lane l of a row holds experts VEC (l + LANES j) .. + VEC - 1.  Returns the lane's sum of D (lane 0 of
+// each row's); nan: some score was a NaN or infinite (such a row's sum is one too, which leaves it to
+// bal_row_alone).
 template <int NJ, int VEC, int R, int LANES>
 __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
   constexpr int kSide = 32 / LANES;
@@ -200,11 +208,12 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
         dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], off);
       }
     float g[R];
-    unsigned skip = 0, rare = 0;  // sets in which this lane's row is not there or left to bal_row_scaled; in
+    unsigned skip = 0, rare = 0;  // sets in which this lane's row is not there or left to bal_row_alone; in
                                   // which some lane's is
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool there = t0 + r * kSide < hi, ok = sum[r] >= kBalSumMin && sum[r] <= kBalSumMax;
+      const bool there = t0 + r * kSide < hi;
+      const bool ok = sum[r] >= kBalSumMin && sum[r] <= kBalSumMax && dot[r] >= -0.5f * sum[r];
       const float inv = 1.f / sum[r];
       dot[r] *= inv;
       g[r] = wq * inv;
@@ -235,7 +244,7 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
       if (!((rare >> r) & 1)) continue;
       const int t = t0 + r * kSide;
       const long long at = (long long)t * p.E;
-      acc += bal_row_scaled<LANES>(p.scores + at, p.dscores ? p.dscores + at : nullptr, p.E, f, wq,
+      acc += bal_row_alone<LANES>(p.scores + at, p.dscores ? p.dscores + at : nullptr, p.E, f, wq,
                                    t < hi && ((skip >> r) & 1), nan);
     }
   }
@@ -243,7 +252,7 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
 }
 
 // The pass over tokens [t0, t1), sequence by sequence (counts known): the block's share of the loss, for
-// thread 0.  f: shared, [E]; wsum: shared, [kBalThreads / 32] doubles.
+// thread 0.  f: shared, [2 kBalMaxE]; wsum: shared, [kBalThreads / 32] doubles.
 template <int NJ, int VEC, int R, int LANES>
 __device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs& sq, int t0, int t1, float* f,
                                            double* wsum) {
@@ -264,7 +273,11 @@ __device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs
     const long long kn = (long long)p.k * (e - b);
     const float per = 1.f / (float)kn, wq = p.coef / ((float)sq.filled * (float)(e - b));
     __syncthreads();  // the sequence before is done with f
-    for (int i = threadIdx.x; i < p.E; i += kBalThreads) f[i] = (float)((long long)p.counts[(long long)q * p.E + i] * p.E - kn) * per;
+    for (int i = threadIdx.x; i < p.E; i += kBalThreads) {
+      const long long c = (long long)p.counts[(long long)q * p.E + i] * p.E;
+      f[i] = (float)(c - kn) * per;
+      f[kBalMaxE + i] = (float)c * per;
+    }
     __syncthreads();
     acc += (double)wq * bal_rows<NJ, VEC, R, LANES>(p, max(b, t0), min(e, t1), f, wq, nan);
   }
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const Balanc
 // The pass of the second form.
 template <int NJ, int VEC, int R, int LANES>
 __global__ void __launch_bounds__(kBalThreads, 2) balance_kernel(const BalanceParams p) {
-  __shared__ __align__(16) float f[1024];
+  __shared__ __align__(16) float f[2 * kBalMaxE];
   __shared__ double wsum[kBalThreads / 32];
   __shared__ BalSeqSmem seqs;
   __shared__ bool last;
@@ -349,7 +362,7 @@ __device__ __forceinline__ double ld_cluster_double(const double* p, uint32_t ra
 template <int NJ, int VEC, int R, int LANES>
 __global__ void __launch_bounds__(kBalThreads, 1) balance_cluster_kernel(const BalanceParams p) {
   __shared__ int hist[kBalHistInts];
-  __shared__ __align__(16) float f[1024];
+  __shared__ __align__(16) float f[2 * kBalMaxE];
   __shared__ double wsum[kBalThreads / 32], total;
   __shared__ BalSeqSmem seqs;
   pdl_wait();

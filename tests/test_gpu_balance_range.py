@@ -9,6 +9,9 @@ R is a sum of at most 32 terms a lane and 5 exchanges: 37 u.  sum s (f - 1): 4 +
 A form that takes D = sum p f as it is has 48 f + 123 D in that place, and where D < 1/2 (so A > 1/2, and
 f <= |f - 1| + 2 A) that is at most 48 |f - 1| + 219 A: 224 u covers both.
   loss sum w D:  84 u A a token, a few roundings of the whole.
+Where D < 1/2 alone, with D = sum p f a sum of non-negative terms: f 4 u, D 4 + 37 + 37 + 1 = 79 u, their
+difference 4 f + 79 D + (f + D), the factors 44 (f + D): 128 u (f + D) w / R covers it, and 84 u of each
+token's D the loss.
 """
 import numpy as np
 import pytest
@@ -100,6 +103,39 @@ def test_small_rows_in_a_batch_of_two_launches(E):
     s[5::7] *= 1e-40
     s[9] = 0
     check(lq.balance_loss(s.cuda(), idx.cuda(), 0.25), s, idx, [0, T], 0.25)
+
+
+@pytest.mark.parametrize("T", [70, 0])
+@pytest.mark.parametrize("small", [1e-3, 1e-7, 1e-12])
+@pytest.mark.parametrize("E,k", [(8, 2), (33, 2), (64, 4), (100, 5), (256, 6), (512, 8), (896, 16), (1023, 3)])
+def test_choices_of_experts_with_small_scores(E, k, small, T):
+    """A batch whose choice (by its biases) fell on experts of small scores: D and the loss are near 0, and the
+    gradient of every other expert is -w D / R.  T = 0: as many tokens as take two launches."""
+    T = T or (1 << 19) // E + 300
+    s, _ = inputs(T, E, k, 5 * E)
+    idx = torch.arange(k, dtype=torch.int32).repeat(T, 1)
+    s[:, :k] *= small
+    out = lq.balance_loss(s.cuda(), idx.cuda(), 0.25)
+    s64 = s.double().numpy()
+    cnt = ob.counts(idx.numpy(), E, [0, T])
+    loss = ob.loss(s64, cnt, k, [0, T], 0.25)
+    g, scale = ob.gradient(s64, cnt, k, [0, T], 0.25)  # scale: w (f + D) / R
+    D = (s64 / s64.sum(1, keepdims=True)) @ (cnt[0] * (E / (k * T)))
+    assert D.max() < 0.49
+    assert abs(float(out["loss"]) - loss) <= 128 * U * loss
+    assert (np.abs(out["dscores"].cpu().double().numpy() - g) <= 128 * U * scale).all()
+
+
+def test_tokens_on_both_sides_of_one_half():
+    """D from 0 to 2 in one batch, its rows side by side in a warp."""
+    T, E, k = 400, 64, 4
+    s, _ = inputs(T, E, k, 77)
+    idx = torch.arange(k, dtype=torch.int32).repeat(T, 1)
+    s[:, :k] *= torch.linspace(0, 1, T)[:, None]
+    for e in (64, 33, 16):
+        part, cu = s[:, :e].contiguous(), [0, 150, T]
+        out = lq.balance_loss(part.cuda(), idx.cuda(), 0.25, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+        check(out, part, idx, cu, 0.25)
 
 
 def test_gradient_past_the_largest_value_is_held_there():
