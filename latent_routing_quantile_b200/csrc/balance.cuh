@@ -117,7 +117,7 @@ constexpr float kBalSumMin = 0x1p-60f, kBalSumMax = 0x1p60f;
 // above as D - 1.  A gradient past fp32 saturates at its largest value; a row of zeros has no
 // probabilities: it adds nothing and gets no gradient.  Returns D in the row's first lane.
 template <int LANES>
-__device__ __forceinline__ float bal_row_alone(const float* srow, float* drow, int E, const float* f, float wq,
+__device__ __forceinline__ double bal_row_alone(const float* srow, float* drow, int E, const float* f, float wq,
                                                 bool there, bool& nan) {
   const int lane = threadIdx.x & (LANES - 1), end = there ? E : 0;
   float top = 0.f;
@@ -151,7 +151,7 @@ __device__ __forceinline__ float bal_row_alone(const float* srow, float* drow, i
       drow[e] = isinf(g) ? copysignf(3.4028234e38f, g) : g;
     }
   }
-  return some && lane == 0 ? (low ? d : 1.f + d) : 0.f;
+  return some && lane == 0 ? (low ? 0.0 : 1.0) + (double)d : 0.0;
 }
 
 // The pass over tokens [lo, hi) of one sequence: f (shared) holds f_qe - 1 and, kBalMaxE further, f_qe.
@@ -160,10 +160,10 @@ __device__ __forceinline__ float bal_row_alone(const float* srow, float* drow, i
 // each row's); nan: some score was a NaN or infinite (such a row's sum is one too, which leaves it to
 // bal_row_alone).
 template <int NJ, int VEC, int R, int LANES>
-__device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
+__device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
   constexpr int kSide = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LANES - 1), side = (threadIdx.x & 31) / LANES;
-  float acc = 0.f;
+  double acc = 0;  // a lane's rows may be thousands, and 1 + (D - 1) drops the low bits of D - 1 in 32 bits
   for (int t0 = lo + warp * R * kSide + side; t0 - side < hi; t0 += kBalThreads / 32 * R * kSide) {
     float s[R][NJ * VEC], sum[R], dot[R];
 #pragma unroll
@@ -217,7 +217,7 @@ __device__ __forceinline__ float bal_rows(const BalanceParams& p, int lo, int hi
       const float inv = 1.f / sum[r];
       dot[r] *= inv;
       g[r] = wq * inv;
-      if (there && ok && lane == 0) acc += 1.f + dot[r];
+      if (there && ok && lane == 0) acc += 1.0 + (double)dot[r];
       if (!there || !ok) skip |= 1u << r;
       if (__any_sync(0xffffffffu, there && !ok)) rare |= 1u << r;
     }
@@ -279,7 +279,7 @@ __device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs
       f[kBalMaxE + i] = (float)c * per;
     }
     __syncthreads();
-    acc += (double)wq * bal_rows<NJ, VEC, R, LANES>(p, max(b, t0), min(e, t1), f, wq, nan);
+    acc += wq * bal_rows<NJ, VEC, R, LANES>(p, max(b, t0), min(e, t1), f, wq, nan);
   }
   if (__any_sync(0xffffffffu, nan) && lane == 0) set_status(p.status, LMOE_STATUS_NAN_SCORE);
 #pragma unroll

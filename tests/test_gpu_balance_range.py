@@ -138,6 +138,30 @@ def test_tokens_on_both_sides_of_one_half():
         check(out, part, idx, cu, 0.25)
 
 
+@pytest.mark.parametrize("equal", [True, False])
+def test_loss_of_tens_of_millions_of_tokens(equal):
+    """A lane sums thousands of rows here: with rows all alike, roundings of a running sum would all fall the
+    same way.  Against a float64 sum on the device, at the bounds of a short batch."""
+    T, E = 1 << 26, 8
+    g = torch.Generator(device="cuda").manual_seed(17)
+    s = torch.rand((1 if equal else T, E), generator=g, device="cuda") + 0.01
+    s = s.expand(T, E).contiguous()
+    idx = torch.randint(0, 5, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    out = lq.balance_loss(s, idx, 0.25, grad=False)
+    cnt = torch.bincount(idx.flatten(), minlength=E)
+    assert torch.equal(out["counts"][0].long(), cnt)
+    f1 = (cnt.double() * E - T) / T
+    loss = slack = 0.0
+    for part in s.split(1 << 22):
+        p = part.double()
+        p /= p.sum(1, keepdim=True)
+        loss += 0.25 / T * float((1 + p @ f1).sum())
+        slack += 0.25 / T * float((p @ f1.abs()).sum())
+    assert abs(float(out["loss"]) - loss) <= 16 * U * loss + 84 * U * slack
+    del s, idx, out, part, p
+    torch.cuda.empty_cache()
+
+
 def test_gradient_past_the_largest_value_is_held_there():
     s = torch.full((2, 8), 2.0 ** -149)
     s[0] = 0.5
