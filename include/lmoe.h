@@ -427,8 +427,9 @@ int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_
  * the step's tokens) stays the caller's, is read by each step and must live as long; the bounds may
  * change between steps, S by another call only.  Bounds that decrease or leave [0, T] set
  * LMOE_STATUS_BAD_INDEX in the handle's status word, and that step has no balance loss.  Layers that
- * lmoe_forward_backward takes only (LMOE_EUNSUPPORTED).  Allocates (about 4 max_tokens E bytes) and
- * synchronises the device: not for a stream capture. */
+ * lmoe_forward_backward takes only (LMOE_EUNSUPPORTED).  Allocates (about 4 max_tokens E bytes; again
+ * for a larger S) and synchronises the device, so that no step reads the bounds of the call before any
+ * more once it returns: not for a stream capture. */
 int lmoe_set_balance(lmoe_handle *h, float coef, const int32_t *cu_seqlens, int32_t S);
 
 /* The last training step's balance loss [1] and counts [S, E] (device, either may be NULL), while

@@ -2026,6 +2026,7 @@ int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int3
   if (!h || !(coef == coef) || S <= 0 || (!cu_seqlens && S != 1) || (uintptr_t)cu_seqlens % 4) return LMOE_EINVAL;
   if (!h->bf || h->q8 || h->q4) return LMOE_EUNSUPPORTED;  // as lmoe_forward_backward
   const size_t Tm = h->cfg.max_tokens, E = h->cfg.E;
+  CK(cudaDeviceSynchronize());  // steps that read the old bounds and use the old buffers
   if (coef != 0.f && h->bal_cap < S) {
     size_t scratch = 0;
     int rc = lmoe_balance_scratch_bytes(&scratch);
@@ -2045,7 +2046,6 @@ int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int3
       return LMOE_ENOMEM;
     }
     for (auto& it : a.items) *it.first = static_cast<uint8_t*>(mem) + it.second;
-    CK(cudaDeviceSynchronize());  // steps that use the old buffers
     cudaFree(h->bal_mem);
     h->bal_mem = mem;
     h->bal_cap = S;
