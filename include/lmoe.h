@@ -425,7 +425,7 @@ int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_
  * scores and choice, with weight coef, to the loss it differentiates (its gradient reaches the router,
  * and through it h and x); coef == 0 takes it out again.  cu_seqlens [S + 1] (NULL: one sequence of all
  * the step's tokens) stays the caller's, is read by each step and must live as long; the bounds may
- * change between steps, S by another call only.  Bounds that decrease or leave [0, T] set
+ * change between steps, S (at most 2^24) by another call only.  Bounds that decrease or leave [0, T] set
  * LMOE_STATUS_BAD_INDEX in the handle's status word, and that step has no balance loss.  Layers that
  * lmoe_forward_backward takes only (LMOE_EUNSUPPORTED).  Allocates (about 4 max_tokens E bytes; again
  * for a larger S) and synchronises the device, so that no step reads the bounds of the call before any

@@ -16,6 +16,8 @@
 
 namespace lmoe {
 
+constexpr int kBalMaxSeqs = 1 << 24;  // sequences of a balance loss
+
 // ------------------------------------------------------------------ tensor maps
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

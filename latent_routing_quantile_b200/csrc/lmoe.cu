@@ -2023,6 +2023,7 @@ int lmoe_set_update(lmoe_handle* h, float beta, uint32_t flags) {
 }
 
 int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int32_t S) {
+  if (S > kBalMaxSeqs) return LMOE_EUNSUPPORTED;
   if (!h || !(coef == coef) || S <= 0 || (!cu_seqlens && S != 1) || (uintptr_t)cu_seqlens % 4) return LMOE_EINVAL;
   if (!h->bf || h->q8 || h->q4) return LMOE_EUNSUPPORTED;  // as lmoe_forward_backward
   const size_t Tm = h->cfg.max_tokens, E = h->cfg.E;

@@ -332,7 +332,7 @@ int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_
                       const int32_t* cu_seqlens, int32_t S, float coef, int32_t* counts, float* loss, float* dscores,
                       void* scratch, uint32_t* status, void* stream) {
   if (T < 0 || E <= 0 || k <= 0 || k > E || S <= 0 || (!cu_seqlens && S != 1) || !(coef == coef)) return LMOE_EINVAL;
-  if (E > kBalMaxE || k > 32 || S > (1 << 24) || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
+  if (E > kBalMaxE || k > 32 || S > kBalMaxSeqs || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
   if (!words(counts) || !words(loss) || !words(status) || !scratch || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
   if (!words(scores, T == 0) || !words(idx, T == 0) || !words(dscores, true) || !words(cu_seqlens, true))
     return LMOE_EINVAL;

@@ -57,3 +57,13 @@ def test_set_balance_returns_once_no_step_reads_the_old_bounds(step):
         step.layer.set_balance(*change)
         assert gate.query()
     assert step.layer.status() == 0
+
+
+def test_more_sequences_than_a_step_takes_are_refused_at_once(step):
+    """Not by the steps, after their forward; the settings before stay."""
+    step.layer.set_balance(1.0)
+    cu = torch.zeros((1 << 24) + 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(lq.LmoeError, match="unsupported"):
+        step.layer.set_balance(1.0, cu)
+    step.run()
+    assert step.layer.balance()[1].shape == (1, 64) and float(step.layer.balance()[0]) > 0
