@@ -433,7 +433,8 @@ int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_
 int lmoe_set_balance(lmoe_handle *h, float coef, const int32_t *cu_seqlens, int32_t S);
 
 /* The last training step's balance loss [1] and counts [S, E] (device, either may be NULL), while
- * lmoe_set_balance has it on. */
+ * lmoe_set_balance has it on: of the last step since that call, zeros before the first (a step of no
+ * tokens changes nothing). */
 int lmoe_get_balance(lmoe_handle *h, float *loss, int32_t *counts, void *stream);
 
 #ifdef __cplusplus

@@ -279,7 +279,7 @@ class Layer:
         self._balance = (cu_seqlens, S)  # the bounds stay alive as long as the steps read them
 
     def balance(self, stream=None):
-        """(loss [1], counts [S, E]) of the last training step with a balance loss."""
+        """(loss [1], counts [S, E]) of the last training step since set_balance; zeros before the first."""
         _, S = getattr(self, "_balance", (None, 1))
         loss = torch.empty(1, dtype=torch.float32, device="cuda")
         counts = torch.empty((S, self.cfg.E), dtype=torch.int32, device="cuda")

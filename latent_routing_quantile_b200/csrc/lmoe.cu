@@ -2055,8 +2055,11 @@ int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int3
     h->bal_counts = counts;
     h->bal_loss = loss;
     h->bal_scratch = scr;
-    CK(cudaMemset(h->bal_loss, 0, 4));
-    CK(cudaMemset(h->bal_counts, 0, (size_t)S * E * 4));
+  }
+  if (coef != 0.f) {  // no step has run with these settings
+    CK(cudaMemsetAsync(h->bal_loss, 0, 4, h->cap));
+    CK(cudaMemsetAsync(h->bal_counts, 0, (size_t)S * E * 4, h->cap));
+    CK(cudaStreamSynchronize(h->cap));
   }
   h->bal_on = coef != 0.f;
   h->bal_coef = coef;

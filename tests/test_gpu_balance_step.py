@@ -67,3 +67,19 @@ def test_more_sequences_than_a_step_takes_are_refused_at_once(step):
         step.layer.set_balance(1.0, cu)
     step.run()
     assert step.layer.balance()[1].shape == (1, 64) and float(step.layer.balance()[0]) > 0
+
+
+def test_no_results_of_steps_before_the_settings(step):
+    """Fewer sequences fit the buffers of more: what balance() gives before the next step is not the old step's
+    counts in another shape."""
+    step.layer.set_balance(1.0, bounds(0, 50, 100, 150, 200, 256))
+    step.run()
+    loss, counts = step.layer.balance()
+    assert float(loss) > 0 and counts.sum(1).tolist() == [200, 200, 200, 200, 224]
+    for change in ((1.0, bounds(0, 100, 256)), (2.0, bounds(0, 100, 256)), (1.0, None)):
+        step.layer.set_balance(*change)
+        loss, counts = step.layer.balance()
+        assert not loss.any() and not counts.any()
+        step.run()
+        loss, counts = step.layer.balance()
+        assert float(loss) > 0 and int(counts.sum()) == 4 * 256
