@@ -432,6 +432,13 @@ int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_
  * more once it returns: not for a stream capture. */
 int lmoe_set_balance(lmoe_handle *h, float coef, const int32_t *cu_seqlens, int32_t S);
 
+/* Data-parallel steps: a loss over all ranks' sequences divides by S' of them all, not by that of a rank's
+ * own.  total (device word, copied on `stream`; 0 counts as NULL) is the S' of the later steps on that
+ * stream: the ranks' losses and gradients then add up to those of one device that saw every token
+ * (sequences cut between ranks count as one on each).  NULL: each step's own S' again, as after
+ * lmoe_set_balance.  LMOE_EINVAL while the loss is off. */
+int lmoe_set_balance_total(lmoe_handle *h, const int32_t *total, void *stream);
+
 /* The last training step's balance loss [1] and counts [S, E] (device, either may be NULL), while
  * lmoe_set_balance has it on: of the last step since that call, zeros before the first (a step of no
  * tokens changes nothing). */

@@ -35,7 +35,8 @@ EXPORTED = (
     "lmoe_profile_enable", "lmoe_profile_read", "lmoe_stage_name", "lmoe_launch_count",
     "lmoe_route_noalloc", "lmoe_watchdog_selftest", "lmoe_gemm_bf16_ex", "lmoe_forward_backward",
     "lmoe_mx4_bytes", "lmoe_mx4_quant", "lmoe_mx4_quant_w13", "lmoe_mx4_dequant", "lmoe_mx4_gemm",
-    "lmoe_balance_scratch_bytes", "lmoe_balance_loss", "lmoe_set_balance", "lmoe_get_balance",
+    "lmoe_balance_scratch_bytes", "lmoe_balance_loss", "lmoe_set_balance", "lmoe_set_balance_total",
+    "lmoe_get_balance",
 )
 NUM_STAGES = 14
 
@@ -104,6 +105,7 @@ def lib() -> ctypes.CDLL:
             "lmoe_mx4_gemm": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i64, u32, vp, vp],
             "lmoe_balance_scratch_bytes": [POINTER(c_size_t)],
             "lmoe_set_balance": [vp, c_float, vp, i32],
+            "lmoe_set_balance_total": [vp, vp, vp],
             "lmoe_get_balance": [vp, vp, vp, vp],
             "lmoe_balance_loss": [vp, vp, i32, i32, i32, vp, i32, c_float, vp, vp, vp, vp, vp, vp],
         }
@@ -172,6 +174,7 @@ class Layer:
                                  ctypes.byref(self.handle)), "lmoe_create")
         (torch.cuda.current_stream() if stream is None else stream).synchronize()
         self._keep = None
+        self._balance = None  # (bounds, sequences) of the balance loss while it is on
         self.last_T = 0
 
     # ---------------------------------------------------------------- forward
@@ -270,17 +273,36 @@ class Layer:
     def set_balance(self, coef, cu_seqlens=None):
         """The router's balance loss in every later forward_backward (weight coef; 0 takes it out), sequence
         by sequence for bounds cu_seqlens (int32 [S + 1] on the device, read at each step; None: the
-        step's tokens are one sequence)."""
+        step's tokens are one sequence).  The loss is a mean over the step's own sequences; dp_train_step
+        makes it one over all ranks'."""
         S = 1
         if cu_seqlens is not None:
             _dev(_offsets(cu_seqlens, "cu_seqlens"), name="cu_seqlens")
             S = cu_seqlens.numel() - 1
         _check(lib().lmoe_set_balance(self.handle, float(coef), _ptr(cu_seqlens), S), "lmoe_set_balance")
-        self._balance = (cu_seqlens, S)  # the bounds stay alive as long as the steps read them
+        # the bounds stay alive as long as the steps read them
+        self._balance = (cu_seqlens, S) if float(coef) != 0 else None
+
+    def balance_sequences(self, T):
+        """Sequences with tokens of a training step of T tokens (int32 [1] on the bounds' device), None while
+        the balance loss is off."""
+        if self._balance is None:
+            return None
+        cu, _ = self._balance
+        if cu is None:
+            return torch.full((1,), int(T > 0), dtype=torch.int32, device="cuda")
+        return (cu[1:] > cu[:-1]).sum(dtype=torch.int32).view(1)
+
+    def set_balance_total(self, total=None, stream=None):
+        """The number of sequences (int32 [1] on the device, copied) that the balance loss of later steps is a
+        mean over: those of all ranks.  None: each step's own again."""
+        if total is not None:
+            _dev(total, torch.int32, (1,), "total")
+        _check(lib().lmoe_set_balance_total(self.handle, _ptr(total), _stream(stream)), "lmoe_set_balance_total")
 
     def balance(self, stream=None):
         """(loss [1], counts [S, E]) of the last training step since set_balance; zeros before the first."""
-        _, S = getattr(self, "_balance", (None, 1))
+        S = 1 if self._balance is None else self._balance[1]
         loss = torch.empty(1, dtype=torch.float32, device="cuda")
         counts = torch.empty((S, self.cfg.E), dtype=torch.int32, device="cuda")
         _check(lib().lmoe_get_balance(self.handle, _ptr(loss), _ptr(counts), _stream(stream)), "lmoe_get_balance")
@@ -444,9 +466,18 @@ def dp_train_step(layer, x, dy, weights, beta=None, literal=False, sign_rule=Fal
     this rank's tokens (QB statistics recorded), then the exchange: every weight gradient summed
     over the ranks with one all-reduce each (the loss is the sum over all ranks' tokens, so its
     gradient is the sum of the ranks' own; dL/dx stays per rank), and, when beta is given, the
-    ranks' QB statistics summed and the bias updated (dp_qb_update).  Returns (y, grads)."""
+    ranks' QB statistics summed and the bias updated (dp_qb_update).  A balance loss (set_balance, on
+    every rank or on none) is a mean over all ranks' sequences, whose number is summed before the
+    step; layer.balance() is then this rank's share of the loss.  Returns (y, grads)."""
     import torch.distributed as dist
+    sequences = getattr(layer, "balance_sequences", None)  # stand-ins may come without the balance loss
+    total = sequences(x.shape[0]) if sequences else None
+    if total is not None:
+        dist.all_reduce(total, group=group)
+        layer.set_balance_total(total, stream)
     y, g = layer.forward_backward(x, dy, weights, record_stats=True, grads=grads, stream=stream)
+    if total is not None:
+        layer.set_balance_total(None, stream)
     for name, t in g.items():
         if name != "x":
             dist.all_reduce(t, group=group)

@@ -35,6 +35,7 @@ struct BalanceParams {
   const int* idx;        // [T, k]
   const int* cu;         // [S + 1] or null (one sequence of all T tokens)
   int T, E, k, S;
+  const int* total;      // [1] or null: S' where it is more than 0 (a batch spread over ranks)
   float coef;
   int* counts;           // [S, E]
   float* loss;           // [1]
@@ -51,7 +52,7 @@ struct BalanceParams {
 constexpr int kBalSeqCache = 1023;
 struct BalSeqs {
   const int* cu;   // shared or global
-  int S, filled;
+  int S, filled;   // sequences; S'
   __device__ __forceinline__ int begin(int q) const { return cu[q]; }
   // The last sequence that begins at or before token t (-1: none does).
   __device__ __forceinline__ int at(int t) const {
@@ -70,6 +71,7 @@ struct BalSeqSmem {
 // The whole block takes part.
 __device__ __forceinline__ BalSeqs bal_seqs(const BalanceParams& p, BalSeqSmem& m) {
   if (threadIdx.x == 0) m.filled = m.bad = 0;
+  const int total = p.total ? *p.total : 0;
   __syncthreads();
   int mine = 0, bad = 0;
   for (int q = threadIdx.x; q < p.S; q += kBalThreads) {
@@ -85,7 +87,7 @@ __device__ __forceinline__ BalSeqs bal_seqs(const BalanceParams& p, BalSeqSmem& 
   if (bad) m.bad = 1;
   __syncthreads();
   if (m.bad && threadIdx.x == 0) set_status(p.status, LMOE_STATUS_BAD_INDEX);
-  return BalSeqs{p.S <= kBalSeqCache ? m.cu : p.cu, m.bad ? 0 : p.S, m.filled};
+  return BalSeqs{p.S <= kBalSeqCache ? m.cu : p.cu, m.bad ? 0 : p.S, total > 0 ? total : m.filled};
 }
 
 // Copies of each of n shared counters: a power of two up to 32, one a lane where there are few, so that

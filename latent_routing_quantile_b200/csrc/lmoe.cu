@@ -380,7 +380,7 @@ struct lmoe_handle {
   int bal_S = 0, bal_cap = 0;  // sequences; those its buffers hold
   void* bal_mem = nullptr;
   float *bal_ds = nullptr, *bal_loss = nullptr, *bal_part = nullptr;
-  int* bal_counts = nullptr;
+  int *bal_counts = nullptr, *bal_total = nullptr;  // bal_total: S' over all ranks, 0 for the step's own
   void* bal_scratch = nullptr;
 };
 
@@ -1520,8 +1520,8 @@ int backward_bf16(lmoe_handle* h, const lmoe_weights* w, const void* x, const vo
     if (rc) return rc;
   }
   if (h->bal_on) {  // the balance loss of this step's scores and choice, and its gradient in the scores
-    int rc = lmoe_balance_loss(h->s, h->idx, T, c.E, c.k, h->bal_cu, h->bal_S, h->bal_coef, h->bal_counts, h->bal_loss,
-                               h->bal_ds, h->bal_scratch, h->status, st);
+    int rc = balance_loss(h->s, h->idx, T, c.E, c.k, h->bal_cu, h->bal_S, h->bal_total, h->bal_coef, h->bal_counts,
+                          h->bal_loss, h->bal_ds, h->bal_scratch, h->status, st);
     if (rc) return rc;
     h->launches += 1;
   }
@@ -2034,12 +2034,13 @@ int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int3
     if (rc) return rc;
     Arena a;
     float *ds, *loss, *part;
-    int* counts;
+    int *counts, *total;
     void* scr;
     a.add((void**)&ds, Tm * E * 4);
     a.add((void**)&part, (Tm + kAuxRows - 1) / kAuxRows * E * 4);
     a.add((void**)&counts, (size_t)S * E * 4);
     a.add((void**)&loss, 4);
+    a.add((void**)&total, 4);
     a.add(&scr, scratch);
     void* mem = nullptr;
     if (cudaMalloc(&mem, a.off) != cudaSuccess) {
@@ -2054,10 +2055,12 @@ int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int3
     h->bal_part = part;
     h->bal_counts = counts;
     h->bal_loss = loss;
+    h->bal_total = total;
     h->bal_scratch = scr;
   }
   if (coef != 0.f) {  // no step has run with these settings
     CK(cudaMemsetAsync(h->bal_loss, 0, 4, h->cap));
+    CK(cudaMemsetAsync(h->bal_total, 0, 4, h->cap));
     CK(cudaMemsetAsync(h->bal_counts, 0, (size_t)S * E * 4, h->cap));
     CK(cudaStreamSynchronize(h->cap));
   }
@@ -2066,6 +2069,14 @@ int lmoe_set_balance(lmoe_handle* h, float coef, const int32_t* cu_seqlens, int3
   h->bal_cu = cu_seqlens;
   h->bal_S = S;
   h->g_bwd.reset(nullptr, nullptr, -1, 0, 0.f, 0);  // captured with the settings before
+  return LMOE_OK;
+}
+
+int lmoe_set_balance_total(lmoe_handle* h, const int32_t* total, void* stream) {
+  if (!h || !h->bal_on || (uintptr_t)total % 4) return LMOE_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (total) CK(cudaMemcpyAsync(h->bal_total, total, 4, cudaMemcpyDeviceToDevice, st));
+  else CK(cudaMemsetAsync(h->bal_total, 0, 4, st));
   return LMOE_OK;
 }
 

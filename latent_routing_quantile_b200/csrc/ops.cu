@@ -148,6 +148,56 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
 
 }  // namespace
 
+int lmoe::balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_t E, int32_t k,
+                       const int32_t* cu_seqlens, int32_t S, const int32_t* total, float coef, int32_t* counts,
+                       float* loss, float* dscores, void* scratch, uint32_t* status, void* stream) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E || S <= 0 || (!cu_seqlens && S != 1) || !(coef == coef)) return LMOE_EINVAL;
+  if (E > kBalMaxE || k > 32 || S > kBalMaxSeqs || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
+  if (!words(counts) || !words(loss) || !words(status) || !scratch || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
+  if (!words(scores, T == 0) || !words(idx, T == 0) || !words(dscores, true) || !words(cu_seqlens, true))
+    return LMOE_EINVAL;
+  int sms = 0;
+  const int rc = device_sms(&sms);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0) {
+    CK(cudaMemsetAsync(counts, 0, (size_t)S * E * sizeof(int32_t), st));
+    CK(cudaMemsetAsync(loss, 0, sizeof(float), st));
+    return LMOE_OK;
+  }
+  BalanceParams p;
+  memset(&p, 0, sizeof(p));
+  p.scores = scores;
+  p.idx = idx;
+  p.cu = cu_seqlens;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.S = S;
+  p.total = total;
+  p.coef = coef;
+  p.counts = counts;
+  p.loss = loss;
+  p.dscores = dscores;
+  p.done = static_cast<unsigned*>(scratch);
+  p.partial = reinterpret_cast<double*>(static_cast<char*>(scratch) + 256);
+  p.status = status;
+  const bool vec = E % 4 == 0 && (((uintptr_t)scores | (uintptr_t)dscores) & 15) == 0;
+  // sets of rows in flight: what fits 64 registers; rows of few experts share a warp (262144 x 8 19 us
+  // against 39 with a row a warp, 65536 x 64 15 against 19)
+  if (vec) {
+    if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st);
+    if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st);
+    if (E <= 128) return launch_balance<1, 4, 4, 32>(p, sms, st);
+    if (E <= 256) return launch_balance<2, 4, 4, 32>(p, sms, st);
+    if (E <= 512) return launch_balance<4, 4, 2, 32>(p, sms, st);
+    return launch_balance<8, 4, 2, 32>(p, sms, st);
+  }
+  if (E <= 64) return launch_balance<2, 1, 4, 32>(p, sms, st);
+  if (E <= 256) return launch_balance<8, 1, 4, 32>(p, sms, st);
+  return launch_balance<32, 1, 1, 32>(p, sms, st);
+}
+
 extern "C" {
 
 int lmoe_mx4_bytes(int64_t rows, int32_t cols, int32_t groups, int32_t ragged, size_t* elem_bytes,
@@ -331,50 +381,8 @@ int lmoe_balance_scratch_bytes(size_t* bytes) {
 int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_t E, int32_t k,
                       const int32_t* cu_seqlens, int32_t S, float coef, int32_t* counts, float* loss, float* dscores,
                       void* scratch, uint32_t* status, void* stream) {
-  if (T < 0 || E <= 0 || k <= 0 || k > E || S <= 0 || (!cu_seqlens && S != 1) || !(coef == coef)) return LMOE_EINVAL;
-  if (E > kBalMaxE || k > 32 || S > kBalMaxSeqs || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
-  if (!words(counts) || !words(loss) || !words(status) || !scratch || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
-  if (!words(scores, T == 0) || !words(idx, T == 0) || !words(dscores, true) || !words(cu_seqlens, true))
-    return LMOE_EINVAL;
-  int sms = 0;
-  const int rc = device_sms(&sms);
-  if (rc) return rc;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (T == 0) {
-    CK(cudaMemsetAsync(counts, 0, (size_t)S * E * sizeof(int32_t), st));
-    CK(cudaMemsetAsync(loss, 0, sizeof(float), st));
-    return LMOE_OK;
-  }
-  BalanceParams p;
-  memset(&p, 0, sizeof(p));
-  p.scores = scores;
-  p.idx = idx;
-  p.cu = cu_seqlens;
-  p.T = T;
-  p.E = E;
-  p.k = k;
-  p.S = S;
-  p.coef = coef;
-  p.counts = counts;
-  p.loss = loss;
-  p.dscores = dscores;
-  p.done = static_cast<unsigned*>(scratch);
-  p.partial = reinterpret_cast<double*>(static_cast<char*>(scratch) + 256);
-  p.status = status;
-  const bool vec = E % 4 == 0 && (((uintptr_t)scores | (uintptr_t)dscores) & 15) == 0;
-  // sets of rows in flight: what fits 64 registers; rows of few experts share a warp (262144 x 8 19 us
-  // against 39 with a row a warp, 65536 x 64 15 against 19)
-  if (vec) {
-    if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st);
-    if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st);
-    if (E <= 128) return launch_balance<1, 4, 4, 32>(p, sms, st);
-    if (E <= 256) return launch_balance<2, 4, 4, 32>(p, sms, st);
-    if (E <= 512) return launch_balance<4, 4, 2, 32>(p, sms, st);
-    return launch_balance<8, 4, 2, 32>(p, sms, st);
-  }
-  if (E <= 64) return launch_balance<2, 1, 4, 32>(p, sms, st);
-  if (E <= 256) return launch_balance<8, 1, 4, 32>(p, sms, st);
-  return launch_balance<32, 1, 1, 32>(p, sms, st);
+  return balance_loss(scores, idx, T, E, k, cu_seqlens, S, nullptr, coef, counts, loss, dscores, scratch, status,
+                      stream);
 }
 
 }  // extern "C"

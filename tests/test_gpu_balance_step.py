@@ -83,3 +83,33 @@ def test_no_results_of_steps_before_the_settings(step):
         step.run()
         loss, counts = step.layer.balance()
         assert float(loss) > 0 and int(counts.sum()) == 4 * 256
+
+
+def test_total_of_all_ranks_scales_the_steps_loss_and_gradient(step):
+    """S' of the whole group in the place of the step's own 2: loss and gradient 2 / 5 of what they were, in
+    steps that replay one graph, until it is taken back."""
+    g0 = {n: t.clone() for n, t in step.run().items()}
+    step.layer.set_balance(2e4, bounds(0, 100, 100, 256))
+    grads = step.run()
+    for _ in range(3):  # eager, captured, replayed
+        step.run(grads=grads)
+    own, (loss, counts) = {n: t.clone() for n, t in grads.items()}, step.layer.balance()
+    for total, share in ((5, 0.4), (1000, 0.002), (None, 1.0), (2, 1.0), (0, 1.0)):
+        step.layer.set_balance_total(None if total is None else torch.tensor([total], dtype=torch.int32, device="cuda"))
+        step.run(grads=grads)
+        got, cnt = step.layer.balance()
+        assert torch.equal(cnt, counts)
+        assert abs(float(got) - share * float(loss)) <= 8 * 2.0 ** -24 * float(loss)
+        for n in ("w_router", "router_bias", "w_down"):
+            # bf16 operands: 2^-8 of the larger of the two gradients' sizes a rounding, two on the way
+            size = float(own[n].abs().max())
+            want = g0[n] + share * (own[n] - g0[n])
+            assert float((grads[n] - want).abs().max()) <= 4 * 2.0 ** -8 * size, (n, total)
+        assert float((own["router_bias"] - g0["router_bias"]).abs().max()) > 0.2 * float(g0["router_bias"].abs().max())
+    step.layer.set_balance_total(torch.tensor([9], dtype=torch.int32, device="cuda"))
+    step.layer.set_balance(2e4, bounds(0, 100, 100, 256))  # its own again
+    step.run(grads=grads)
+    assert abs(float(step.layer.balance()[0]) - float(loss)) <= 8 * 2.0 ** -24 * float(loss)
+    step.layer.set_balance(0.0)
+    with pytest.raises(lq.LmoeError, match="invalid"):
+        step.layer.set_balance_total(None)
