@@ -6,6 +6,7 @@ import of the binding still works, but the first call raises: there is no CPU fa
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -431,6 +432,11 @@ def gemm_bf16_ex(a, b, a_mn=False, b_mn=False, k_split=1, stream=None):
     return c
 
 
+def _current(stream):
+    """Makes `stream` (None: no change) the current one, which collectives are ordered by."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def sum_qb_statistics(hist, ntok, load=None, group=None):
     """The data-parallel exchange step of the bias update: sums the integer histograms [E, 4096],
     token counts and (for the sign rule) expert loads [E] of all ranks in place (torch.distributed
@@ -451,13 +457,14 @@ def dp_qb_update(layer, beta, literal=False, sign_rule=False, group=None, stream
     rank then applies the update one device would apply after seeing every rank's tokens, and all
     ranks keep the same bias ("Pretraining a Mini Kimi K3", capsule 27, Bug 2: the all-reduce
     comes before the update)."""
-    hist, n = layer.hist(stream)
-    load = layer.load(stream) if sign_rule else None
-    sum_qb_statistics(hist, n, load, group)
-    layer.set_hist(hist, n, stream)
-    if load is not None:
-        layer.set_load(load, stream)
-    layer.qb_update(beta, literal=literal, sign_rule=sign_rule, stream=stream)
+    with _current(stream):
+        hist, n = layer.hist(stream)
+        load = layer.load(stream) if sign_rule else None
+        sum_qb_statistics(hist, n, load, group)
+        layer.set_hist(hist, n, stream)
+        if load is not None:
+            layer.set_load(load, stream)
+        layer.qb_update(beta, literal=literal, sign_rule=sign_rule, stream=stream)
 
 
 def dp_train_step(layer, x, dy, weights, beta=None, literal=False, sign_rule=False, group=None, grads=None,
@@ -471,16 +478,17 @@ def dp_train_step(layer, x, dy, weights, beta=None, literal=False, sign_rule=Fal
     step; layer.balance() is then this rank's share of the loss.  Returns (y, grads)."""
     import torch.distributed as dist
     sequences = getattr(layer, "balance_sequences", None)  # stand-ins may come without the balance loss
-    total = sequences(x.shape[0]) if sequences else None
-    if total is not None:
-        dist.all_reduce(total, group=group)
-        layer.set_balance_total(total, stream)
-    y, g = layer.forward_backward(x, dy, weights, record_stats=True, grads=grads, stream=stream)
-    if total is not None:
-        layer.set_balance_total(None, stream)
-    for name, t in g.items():
-        if name != "x":
-            dist.all_reduce(t, group=group)
+    with _current(stream):
+        total = sequences(x.shape[0]) if sequences else None
+        if total is not None:
+            dist.all_reduce(total, group=group)
+            layer.set_balance_total(total, stream)
+        y, g = layer.forward_backward(x, dy, weights, record_stats=True, grads=grads, stream=stream)
+        if total is not None:
+            layer.set_balance_total(None, stream)
+        for name, t in g.items():
+            if name != "x":
+                dist.all_reduce(t, group=group)
     if beta is not None:
         dp_qb_update(layer, beta, literal=literal, sign_rule=sign_rule, group=group, stream=stream)
     return y, g

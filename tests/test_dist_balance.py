@@ -118,3 +118,36 @@ def test_no_exchange_without_a_balance_loss():
     layer = BalanceLayer(None, [0, 1])
     layer._balance = None
     assert layer.balance_sequences(9) is None
+
+
+def test_collectives_follow_the_named_stream(monkeypatch):
+    """On a stream that the caller names, every collective and every tensor made for one is issued with that
+    stream current: the sums would otherwise not wait for the step that writes what they sum."""
+    import contextlib
+    current, seen = ["default"], []
+
+    @contextlib.contextmanager
+    def make_current(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    class Recorder:
+        def __getattr__(self, name):
+            def call(*args, **kw):
+                seen.append((name, current[-1], kw.get("stream", args[-1] if args else None)))
+                if name == "forward_backward":
+                    return None, {"x": torch.zeros(1), "w_up": torch.zeros(1)}
+                if name in ("hist", "load"):
+                    return (torch.zeros(1), torch.zeros(1)) if name == "hist" else torch.zeros(1)
+                return torch.zeros(1)
+            return call
+
+    monkeypatch.setattr(torch.cuda, "stream", make_current)
+    monkeypatch.setattr(dist, "all_reduce", lambda t, group=None: seen.append(("all_reduce", current[-1], "side")))
+    lq.dp_train_step(Recorder(), torch.zeros(4, 8), None, None, beta=0.1, sign_rule=True, stream="side")
+    assert [n for n, _, _ in seen].count("all_reduce") == 1 + 1 + 3
+    assert all(c == "side" for _, c, _ in seen), seen
+    seen.clear()
+    lq.dp_train_step(Recorder(), torch.zeros(4, 8), None, None, beta=0.1)
+    assert all(c == "default" for _, c, _ in seen)

@@ -113,3 +113,31 @@ def test_total_of_all_ranks_scales_the_steps_loss_and_gradient(step):
     step.layer.set_balance(0.0)
     with pytest.raises(lq.LmoeError, match="invalid"):
         step.layer.set_balance_total(None)
+
+
+def test_data_parallel_step_of_one_rank_on_a_named_stream(step):
+    """dp_train_step with a balance loss in a group of one: the step's own gradients and loss."""
+    import datetime
+    import socket
+    import torch.distributed as dist
+    step.layer.set_balance(2e4, bounds(0, 100, 100, 256))
+    ref = step.run()
+    loss = float(step.layer.balance()[0])
+    torch.cuda.synchronize()
+    with socket.socket() as s:
+        s.bind(("127.0.0.1", 0))
+        port = s.getsockname()[1]
+    dist.init_process_group("nccl", init_method=f"tcp://127.0.0.1:{port}", rank=0, world_size=1,
+                            timeout=datetime.timedelta(seconds=120))
+    try:
+        side = torch.cuda.Stream()
+        for stream in (None, side):
+            _, g = lq.dp_train_step(step.layer, step.x, step.dy, step.w_dev, beta=0.01, stream=stream)
+            torch.cuda.synchronize()
+            assert abs(float(step.layer.balance()[0]) - loss) <= 2.0 ** -20 * loss
+            step.layer.set_bias(torch.zeros(64, device="cuda"))
+            for n in ref:
+                # sums over K ranges in another order: the last bits
+                assert torch.allclose(g[n], ref[n], rtol=1e-4, atol=1e-4 * float(ref[n].abs().max())), n
+    finally:
+        dist.destroy_process_group()
