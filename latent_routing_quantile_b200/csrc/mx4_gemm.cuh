@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
           ok = false;
           break;
         }
+        tc_fence_after();  // the MMAs that last read these columns committed before the stage was loaded again
         const uint8_t* s_src = smem + stage * C::kStageBytes + C::kABytes + C::kBBytes + 16 * lane;
         const uint32_t t = tq + stage * C::kSfBuf;
         uint4 v[2 + BN / 64];

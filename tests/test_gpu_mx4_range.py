@@ -1,0 +1,45 @@
+"""MXFP4 quantisation and products at the ends of their ranges of sizes, against exact values."""
+import numpy as np
+import pytest
+import torch
+
+import latent_routing_quantile_b200 as lq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from latent_routing_quantile_b200 import build
+    build.build()
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    assert lq.op_status() == 0
+
+
+def whole_numbers(rows, cols, seed):
+    """Codes 1 .. 6 of either sign times 1, 2 or 4, block by block: MXFP4 holds each exactly."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.tensor([1.0, 2.0, 3.0, 4.0, 6.0], device="cuda")
+    v = q[torch.randint(0, 5, (rows, cols), generator=g, device="cuda")]
+    v[:, ::32] = 4.0
+    v *= torch.randint(0, 2, (rows, cols), generator=g, device="cuda") * 2 - 1
+    s = torch.exp2(torch.randint(0, 3, (rows, cols // 32), generator=g, device="cuda").float())
+    return (v * s.repeat_interleave(32, dim=1)).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 8192, 8192), (1024, 4100, 4128), (100, 300, 8192)])
+def test_every_k_block_takes_its_own_scales(M, N, K):
+    """The scales of one stage of the ring after another pass through the same tensor memory, many times a tile
+    and in several tiles a CTA.  Whole numbers whose sums stay below 36 16 8192 < 2^24: equal to the bit."""
+    a, b = whole_numbers(M, K, M + K), whole_numbers(N, K, N)
+    ref = (a.double() @ b.double().t()).float()
+    qa, qb = lq.mx4_quant(a), lq.mx4_quant(b)
+    for _ in range(10):
+        assert torch.equal(lq.mx4_gemm(qa, qb, dtype=torch.float32), ref)
