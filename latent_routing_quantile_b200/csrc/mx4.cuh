@@ -27,7 +27,7 @@ namespace lmoe {
 
 constexpr int kMx4MaxGroups = 1024;
 
-__host__ __device__ __forceinline__ int mx4_kblocks(int cols) { return (cols + 255) / 256; }
+__host__ __device__ __forceinline__ int mx4_kblocks(int cols) { return cols / 256 + (cols % 256 != 0); }
 
 // How the rows of a matrix fall into groups.
 struct Mx4Rows {

@@ -43,3 +43,19 @@ def test_every_k_block_takes_its_own_scales(M, N, K):
     qa, qb = lq.mx4_quant(a), lq.mx4_quant(b)
     for _ in range(10):
         assert torch.equal(lq.mx4_gemm(qa, qb, dtype=torch.float32), ref)
+
+
+def test_a_row_of_two_billion_columns():
+    """The widest matrix an int32 of columns allows: its ends and middle come out as they do alone."""
+    cols = (1 << 31) - 32
+    x = torch.empty((1, cols), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for part in x.split(1 << 27, dim=1):
+        part.normal_(generator=g)
+    q = lq.mx4_quant(x)
+    v = lq.mx4_dequant(q)
+    for at in (0, 1 << 20, (1 << 30) - 512, cols - 992 - 32):
+        part = x[:, at:at + 1024]
+        assert torch.equal(v[:, at:at + 1024], lq.mx4_dequant(lq.mx4_quant(part)))
+    del x, q, v, part
+    torch.cuda.empty_cache()

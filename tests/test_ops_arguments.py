@@ -21,3 +21,18 @@ def L():
 def test_set_balance_refuses_more_sequences_than_its_steps_take(L):
     assert L.lmoe_set_balance(None, 0.1, P, (1 << 24) + 1) == EUNSUPPORTED
     assert L.lmoe_set_balance(None, 0.1, P, 1 << 24) == EINVAL  # no handle
+
+
+def _bytes(L, rows, cols, groups, ragged):
+    e, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    return L.lmoe_mx4_bytes(rows, cols, groups, ragged, ctypes.byref(e), ctypes.byref(s)), e.value, s.value
+
+
+def test_sizes_of_the_widest_rows(L):
+    """cols up to the last multiple of 32 that an int32 holds: k-blocks of 256 are counted without overflow."""
+    cols = (1 << 31) - 32
+    assert _bytes(L, 1, cols, 1, 0) == (0, cols // 2, 1024 * (1 << 23))
+    assert _bytes(L, 128, cols - 192, 1, 1) == (0, 128 * ((cols - 192) // 2), 2 * 1024 * ((1 << 23) - 1) + 2 * 1024)
+    # 2^23 k-blocks of 8 slices a tile: 31 tiles stay below 2^31 slices, 32 do not
+    assert _bytes(L, 31 * 128, cols, 1, 0)[0] == 0
+    assert _bytes(L, 31 * 128 + 1, cols, 1, 0)[0] == EUNSUPPORTED
