@@ -278,8 +278,10 @@ class Layer:
         makes it one over all ranks'."""
         S = 1
         if cu_seqlens is not None:
-            _dev(_offsets(cu_seqlens, "cu_seqlens"), name="cu_seqlens")
-            S = cu_seqlens.numel() - 1
+            S = _offsets(cu_seqlens, "cu_seqlens").numel() - 1
+            if S > _INT_MAX:
+                _too_large(S=S)
+            _dev(cu_seqlens, name="cu_seqlens")
         _check(lib().lmoe_set_balance(self.handle, float(coef), _ptr(cu_seqlens), S), "lmoe_set_balance")
         # the bounds stay alive as long as the steps read them
         self._balance = (cu_seqlens, S) if float(coef) != 0 else None
@@ -590,6 +592,15 @@ class _Elsewhere:
         return False
 
 
+_INT_MAX = 0x7fffffff
+
+
+def _too_large(**sizes):
+    """Raises for sizes that the C entries' 32-bit arguments do not hold (ctypes would drop their upper bits)."""
+    names = ", ".join(f"{n} = {v}" for n, v in sizes.items() if v > _INT_MAX)
+    raise LmoeError(f"unsupported shape: {names} is more than {_INT_MAX}")
+
+
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
@@ -675,6 +686,8 @@ def mx4_quant(x, offsets=None, index=None, out=None, stream=None) -> Mx4:
         rows, cols, ld = groups * shape[1], shape[2], shape[2]
     else:
         raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets and index")
+    if cols > _INT_MAX or groups > _INT_MAX:
+        _too_large(cols=cols, groups=groups)
     dev = _device_of(x, offsets, index, None if out is None else out.buf)
     if stream is not None or dev != _current_device():
         with _Elsewhere(dev, stream, x, offsets, index, None if out is None else out.buf):
@@ -703,6 +716,8 @@ def mx4_quant_w13(w1, w3, out=None, stream=None) -> Mx4:
     stacked = w1.dim() == 3
     groups = w1.shape[0] if stacked else 1
     h, cols = w1.shape[-2:]
+    if max(groups, h, cols) > _INT_MAX:
+        _too_large(groups=groups, h=h, cols=cols)
     dev = _device_of(w1, w3, None if out is None else out.buf)
     if stream is not None or dev != _current_device():
         with _Elsewhere(dev, stream, w1, w3, None if out is None else out.buf):
@@ -799,6 +814,8 @@ def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream
     S = 1
     if cu_seqlens is not None:
         S = _offsets(cu_seqlens, "cu_seqlens").numel() - 1
+    if max(T, E, k, S) > _INT_MAX:
+        _too_large(T=T, E=E, k=k, S=S)
     dev = _device_of(scores, idx, cu_seqlens)
     _dev(scores, torch.float32, None, "scores")
     _dev(idx, torch.int32, (T, k), "idx")

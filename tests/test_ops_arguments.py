@@ -36,3 +36,42 @@ def test_sizes_of_the_widest_rows(L):
     # 2^23 k-blocks of 8 slices a tile: 31 tiles stay below 2^31 slices, 32 do not
     assert _bytes(L, 31 * 128, cols, 1, 0)[0] == 0
     assert _bytes(L, 31 * 128 + 1, cols, 1, 0)[0] == EUNSUPPORTED
+
+
+def _of(shape, dtype):
+    """A tensor of any shape on the meta device: no memory."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def test_sizes_past_32_bits_are_refused_not_cut():
+    """2^32 + 32 columns are not 32 columns."""
+    big, bf = (1 << 32) + 32, torch.bfloat16
+    calls = [lambda: lq.mx4_quant(_of((1, big), bf)),
+             lambda: lq.mx4_quant(_of((big, 1, 64), bf)),
+             lambda: lq.mx4_quant(_of((1, 64), bf), offsets=_of((big,), torch.int32)),
+             lambda: lq.mx4_quant_w13(*(_CudaLike((64, big)) for _ in range(2))),
+             lambda: lq.mx4_quant_w13(*(_CudaLike((big, 32)) for _ in range(2))),
+             lambda: lq.balance_loss(_of((big, 8), torch.float32), _of((big, 2), torch.int32), 0.1),
+             lambda: lq.balance_loss(_of((8, 8), torch.float32), _of((8, 2), torch.int32), 0.1,
+                                     cu_seqlens=_of((big,), torch.int32)),
+             lambda: lq.Layer.set_balance(lq.Layer.__new__(lq.Layer), 0.1, _of((big,), torch.int32))]
+    for call in calls:
+        with pytest.raises(lq.LmoeError, match="unsupported shape"):
+            call()
+
+
+class _CudaLike:
+    """What mx4_quant_w13 looks at before its sizes."""
+    dtype, is_cuda = torch.bfloat16, True
+
+    def __init__(self, shape):
+        self.shape = torch.Size(shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
