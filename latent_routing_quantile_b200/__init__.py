@@ -844,6 +844,8 @@ def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream
         else:
             res["dscores"] = torch.empty_like(scores)
         dscores = res["dscores"].data_ptr()
+    else:
+        res.pop("dscores", None)  # a given one is not this call's
     rc = lib().lmoe_balance_loss(scores.data_ptr(), idx.data_ptr(), T, E, k,
                                  None if cu_seqlens is None else cu_seqlens.data_ptr(), S, coef,
                                  res["counts"].data_ptr(), res["loss"].data_ptr(), dscores, buf.data_ptr() + 64,

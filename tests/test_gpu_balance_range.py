@@ -162,6 +162,18 @@ def test_loss_of_tens_of_millions_of_tokens(equal):
     torch.cuda.empty_cache()
 
 
+def test_no_gradient_is_returned_that_was_not_made():
+    """grad=False with the buffers of an earlier call: its gradient is left alone and not handed on."""
+    s, idx = inputs(50, 64, 4, 41)
+    out = lq.balance_loss(s.cuda(), idx.cuda(), 0.25)
+    s2, idx2 = inputs(50, 64, 4, 42)
+    old = out["dscores"].clone()
+    again = lq.balance_loss(s2.cuda(), idx2.cuda(), 0.25, grad=False, out=out)
+    assert sorted(again) == ["counts", "loss"] and torch.equal(out["dscores"], old)
+    assert again["loss"] is out["loss"]
+    check({**again, "dscores": lq.balance_loss(s2.cuda(), idx2.cuda(), 0.25)["dscores"]}, s2, idx2, [0, 50], 0.25)
+
+
 def test_gradient_past_the_largest_value_is_held_there():
     s = torch.full((2, 8), 2.0 ** -149)
     s[0] = 0.5
