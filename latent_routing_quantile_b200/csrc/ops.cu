@@ -218,7 +218,8 @@ int lmoe_mx4_quant(const void* x, int32_t dtype, int64_t ld, const int32_t* inde
   if (dtype != LMOE_F32 && dtype != LMOE_BF16) return LMOE_EINVAL;
   if (index && (x_rows < 0 || x_rows > INT32_MAX)) return LMOE_EINVAL;
   if (rows == 0) return LMOE_OK;
-  if (!x || !elems || !scales || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15)) return LMOE_EINVAL;
+  if (!x && !(index && x_rows == 0)) return LMOE_EINVAL;  // every index is outside an x without rows
+  if (!elems || !scales || ld < cols || ((uintptr_t)elems & 15) || ((uintptr_t)scales & 15)) return LMOE_EINVAL;
   if (!words(status) || !words(offsets, true) || !words(index, true)) return LMOE_EINVAL;
   if ((uintptr_t)x % (dtype == LMOE_F32 ? 4 : 2)) return LMOE_EINVAL;
   int sms = 0;

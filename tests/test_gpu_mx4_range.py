@@ -59,3 +59,15 @@ def test_a_row_of_two_billion_columns():
         assert torch.equal(v[:, at:at + 1024], lq.mx4_dequant(lq.mx4_quant(part)))
     del x, q, v, part
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_indexed_rows_of_a_batch_without_tokens(dtype):
+    """No index is inside: rows of zeros, reported (as for any index outside x), not a refused call."""
+    q = lq.mx4_quant(torch.empty(0, 96, dtype=dtype, device="cuda"),
+                     index=torch.tensor([0, -1, 5], dtype=torch.int32, device="cuda"))
+    assert lq.op_status() == lq.STATUS_BAD_INDEX
+    v = lq.mx4_dequant(q)
+    assert v.shape == (3, 96) and not v.any()
+    none = lq.mx4_quant(torch.empty(0, 96, dtype=dtype, device="cuda"), index=torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert none.rows == 0
