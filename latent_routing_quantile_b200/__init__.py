@@ -534,26 +534,36 @@ def _status_word(index: int) -> int:
     w = _status_words.get(index)
     if w is None:
         if torch.cuda.is_current_stream_capturing():
-            raise LmoeError("the first operator call on a device cannot be captured: make one before the capture")
+            raise LmoeError("the first operator call on a device cannot be captured: make one before the capture, "
+                            "or pass a status word")
         word = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
         torch.cuda.synchronize(index)
         w = _status_words.setdefault(index, (word, word.data_ptr()))  # of two threads' words the first stays
     return w[1]
 
 
+def _status_at(status, index: int) -> int:
+    """Address of a call's status word: the caller's own, or the device's."""
+    if status is None:
+        return _status_word(index)
+    return _dev(status, torch.int32, (1,), "status").data_ptr()
+
+
 def op_status(device=None) -> int:
     """Fault bits (STATUS_*) of the mx4_* and balance_loss calls on `device` since the last read;
-    synchronises the device and clears them."""
+    synchronises the device and clears the bits it returns.  Every thread's and stream's calls share
+    them, but for calls with a word of their own (status=, int32 [1] on the device: the call ORs its
+    bits in and never clears them)."""
     index = None if device is None else torch.device(device).index
     index = torch.cuda.current_device() if index is None else index
     if index not in _status_words:
         return 0
     word = _status_words[index][0]
     torch.cuda.synchronize(index)
-    v = int(word.item()) & 0xffffffff
-    word.zero_()
+    v = int(word.item())
+    word.bitwise_and_(~v)  # a bit that another thread's call set in between stays
     torch.cuda.synchronize(index)
-    return v
+    return v & 0xffffffff
 
 
 def _device_of(*tensors) -> int:
@@ -655,11 +665,11 @@ class Mx4:
         self.offsets = offsets
 
 
-def mx4_quant(x, offsets=None, index=None, out=None, stream=None) -> Mx4:
+def mx4_quant(x, offsets=None, index=None, out=None, stream=None, status=None) -> Mx4:
     """x in MXFP4: [rows, cols] (fp32 or bf16, cols a multiple of 32, any row stride), or stacked
     matrices [groups, rows, cols].  index (int32 [n]): the n rows x[index] instead, as routing's perm
     names them.  offsets (int32 [groups + 1]): the rows' groups, for the grouped product.  out: an
-    Mx4 of an earlier call with the same shapes, to write into."""
+    Mx4 of an earlier call with the same shapes, to write into.  status: see op_status."""
     dt = _dtype(x.dtype, "x")
     shape = x.shape
     x_rows = 0
@@ -688,10 +698,10 @@ def mx4_quant(x, offsets=None, index=None, out=None, stream=None) -> Mx4:
         raise LmoeError("x must be [rows, cols], or [groups, rows, cols] without offsets and index")
     if cols > _INT_MAX or groups > _INT_MAX:
         _too_large(cols=cols, groups=groups)
-    dev = _device_of(x, offsets, index, None if out is None else out.buf)
+    dev = _device_of(x, offsets, index, None if out is None else out.buf, status)
     if stream is not None or dev != _current_device():
-        with _Elsewhere(dev, stream, x, offsets, index, None if out is None else out.buf):
-            return mx4_quant(x, offsets, index, out)
+        with _Elsewhere(dev, stream, x, offsets, index, None if out is None else out.buf, status):
+            return mx4_quant(x, offsets, index, out, status=status)
     if out is None:
         out = Mx4(rows, cols, groups, offsets, stacked, x)
     else:
@@ -699,13 +709,13 @@ def mx4_quant(x, offsets=None, index=None, out=None, stream=None) -> Mx4:
     elems, scales = out._ptrs()
     rc = lib().lmoe_mx4_quant(x.data_ptr(), dt, ld, None if index is None else index.data_ptr(), x_rows, rows, cols,
                               groups, None if offsets is None else offsets.data_ptr(), elems, scales,
-                              _status_word(dev), _raw_stream(dev))
+                              _status_at(status, dev), _raw_stream(dev))
     if rc:
         _check(rc, "lmoe_mx4_quant")
     return out
 
 
-def mx4_quant_w13(w1, w3, out=None, stream=None) -> Mx4:
+def mx4_quant_w13(w1, w3, out=None, stream=None, status=None) -> Mx4:
     """A SwiGLU's gate and linear projections w1, w3 ([h, cols] or stacked [groups, h, cols], h a
     multiple of 64) as one MXFP4 matrix for mx4_gemm(..., swiglu=True)."""
     dt = _dtype(w1.dtype, "w1")
@@ -718,21 +728,21 @@ def mx4_quant_w13(w1, w3, out=None, stream=None) -> Mx4:
     h, cols = w1.shape[-2:]
     if max(groups, h, cols) > _INT_MAX:
         _too_large(groups=groups, h=h, cols=cols)
-    dev = _device_of(w1, w3, None if out is None else out.buf)
+    dev = _device_of(w1, w3, None if out is None else out.buf, status)
     if stream is not None or dev != _current_device():
-        with _Elsewhere(dev, stream, w1, w3, None if out is None else out.buf):
-            return mx4_quant_w13(w1, w3, out)
+        with _Elsewhere(dev, stream, w1, w3, None if out is None else out.buf, status):
+            return mx4_quant_w13(w1, w3, out, status=status)
     if out is None:
         out = Mx4(2 * groups * h, cols, groups, None, stacked, w1, glu=True)
     else:
         out._match(2 * groups * h, cols, groups, None, stacked, True)
     elems, scales = out._ptrs()
     _check(lib().lmoe_mx4_quant_w13(w1.data_ptr(), w3.data_ptr(), dt, groups, h, cols, elems, scales,
-                                    _status_word(dev), _raw_stream(dev)), "lmoe_mx4_quant_w13")
+                                    _status_at(status, dev), _raw_stream(dev)), "lmoe_mx4_quant_w13")
     return out
 
 
-def mx4_dequant(q: Mx4, dtype=torch.bfloat16, out=None, stream=None):
+def mx4_dequant(q: Mx4, dtype=torch.bfloat16, out=None, stream=None, status=None):
     """The values q stands for, [rows, cols] (stacked matrices: [groups, rows / groups, cols]).
     Rows of q that belong to no group: zeros, or left as they are in a given `out`."""
     dt = _dtype(dtype if out is None else out.dtype, "dtype")
@@ -740,22 +750,22 @@ def mx4_dequant(q: Mx4, dtype=torch.bfloat16, out=None, stream=None):
     if out is not None and (tuple(out.shape) != shape or not out.is_contiguous()):
         raise LmoeError(f"out must be contiguous and have shape {shape}")
     offsets = q.offsets
-    dev = _device_of(q.buf, offsets, out)
+    dev = _device_of(q.buf, offsets, out, status)
     if stream is not None or dev != _current_device():
-        with _Elsewhere(dev, stream, q.buf, offsets, out):
-            return mx4_dequant(q, dtype, out)
+        with _Elsewhere(dev, stream, q.buf, offsets, out, status):
+            return mx4_dequant(q, dtype, out, status=status)
     flags = 0
     if out is None:
         out, flags = torch.empty(shape, dtype=dtype, device=q.buf.device), MX4_ZERO_REST
     elems, scales = q._ptrs()
     rc = lib().lmoe_mx4_dequant(elems, scales, q.rows, q.cols, q.groups, None if offsets is None else offsets.data_ptr(),
-                                out.data_ptr(), dt, q.cols, flags, _status_word(dev), _raw_stream(dev))
+                                out.data_ptr(), dt, q.cols, flags, _status_at(status, dev), _raw_stream(dev))
     if rc:
         _check(rc, "lmoe_mx4_dequant")
     return out
 
 
-def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, stream=None):
+def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, stream=None, status=None):
     """a b^T of MXFP4 matrices with fp32 sums: [M, N] in fp32 or bf16.  b stacked [groups, N, K]: a
     quantised with offsets, its rows of group g times matrix g.  swiglu=True: b from mx4_quant_w13,
     the result bf16 silu(gate) * linear [M, N / 2].  Rows of a that belong to no group: zeros, or
@@ -775,10 +785,10 @@ def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, strea
     if out is not None and (tuple(out.shape) != (M, cols) or (cols > 1 and out.stride(1) != 1) or
                             (M > 1 and out.stride(0) < cols)):
         raise LmoeError(f"out must have shape {(M, cols)}, contiguous columns and rows that do not overlap")
-    dev = _device_of(a.buf, offsets, b.buf, out)
+    dev = _device_of(a.buf, offsets, b.buf, out, status)
     if stream is not None or dev != _current_device():
-        with _Elsewhere(dev, stream, a.buf, offsets, b.buf, out):
-            return mx4_gemm(a, b, swiglu, dtype, out)
+        with _Elsewhere(dev, stream, a.buf, offsets, b.buf, out, status):
+            return mx4_gemm(a, b, swiglu, dtype, out, status=status)
     flags = MX4_SWIGLU if swiglu else 0
     ld = cols
     if out is None:
@@ -788,7 +798,7 @@ def mx4_gemm(a: Mx4, b: Mx4, swiglu=False, dtype=torch.bfloat16, out=None, strea
     ae, asc = a._ptrs()
     be, bsc = b._ptrs()
     rc = lib().lmoe_mx4_gemm(ae, asc, be, bsc, M, N, a.cols, a.groups, None if offsets is None else offsets.data_ptr(),
-                             out.data_ptr(), dt, ld, flags, _status_word(dev), _raw_stream(dev))
+                             out.data_ptr(), dt, ld, flags, _status_at(status, dev), _raw_stream(dev))
     if rc:
         _check(rc, "lmoe_mx4_gemm")
     return out
@@ -802,11 +812,11 @@ def _balance_floats() -> int:
     return 16 + (n.value + 3) // 4
 
 
-def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream=None):
+def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream=None, status=None):
     """Balance loss of a router (lmoe_balance_loss): scores [T, E] fp32 and the choice idx [T, k] int32,
     as Layer.routing() gives them; cu_seqlens (int32 [S + 1]) bounds the sequences (None: one).
     Returns dict(loss [1] fp32, counts [S, E] int32, dscores [T, E] fp32): the gradient of the loss
-    in the scores, left out with grad=False.  `out` may pass preallocated buffers."""
+    in the scores, left out with grad=False.  `out` may pass preallocated buffers.  status: see op_status."""
     if scores.dim() != 2 or idx.dim() != 2:
         raise LmoeError("scores must be [T, E] and idx [T, k]")
     T, E = scores.shape
@@ -816,13 +826,13 @@ def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream
         S = _offsets(cu_seqlens, "cu_seqlens").numel() - 1
     if max(T, E, k, S) > _INT_MAX:
         _too_large(T=T, E=E, k=k, S=S)
-    dev = _device_of(scores, idx, cu_seqlens)
+    dev = _device_of(scores, idx, cu_seqlens, status)
     _dev(scores, torch.float32, None, "scores")
     _dev(idx, torch.int32, (T, k), "idx")
     given = () if out is None else tuple(out.values())
     if stream is not None or dev != _current_device():
-        with _Elsewhere(dev, stream, scores, idx, cu_seqlens, *given):
-            return balance_loss(scores, idx, coef, cu_seqlens, grad, out)
+        with _Elsewhere(dev, stream, scores, idx, cu_seqlens, status, *given):
+            return balance_loss(scores, idx, coef, cu_seqlens, grad, out, status=status)
     if given:
         _device_of(scores, *given)
     device = scores.device
@@ -849,7 +859,7 @@ def balance_loss(scores, idx, coef, cu_seqlens=None, grad=True, out=None, stream
     rc = lib().lmoe_balance_loss(scores.data_ptr(), idx.data_ptr(), T, E, k,
                                  None if cu_seqlens is None else cu_seqlens.data_ptr(), S, coef,
                                  res["counts"].data_ptr(), res["loss"].data_ptr(), dscores, buf.data_ptr() + 64,
-                                 _status_word(dev), _raw_stream(dev))
+                                 _status_at(status, dev), _raw_stream(dev))
     if rc:
         _check(rc, "lmoe_balance_loss")
     return res

@@ -75,3 +75,18 @@ class _CudaLike:
 
     def is_contiguous(self):
         return True
+
+
+def test_op_status_clears_only_the_bits_it_returns(monkeypatch):
+    """A bit that another thread's call sets between the read and the clearing is there for the next read."""
+    class Word(torch.Tensor):
+        def item(self):
+            v = super().item()
+            self.bitwise_or_(lq.STATUS_BAD_INDEX)
+            return v
+
+    word = torch.tensor([lq.STATUS_NAN_SCORE], dtype=torch.int32).as_subclass(Word)
+    monkeypatch.setattr(lq, "_status_words", {0: (word, word.data_ptr())})
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda index=None: None)
+    assert lq.op_status(torch.device("cuda", 0)) == lq.STATUS_NAN_SCORE
+    assert lq.op_status(torch.device("cuda", 0)) == lq.STATUS_BAD_INDEX
