@@ -46,6 +46,17 @@ struct BalanceParams {
   int chunk;             // tokens a block
 };
 
+// CTAs of the one-launch form, at most `most`: a round of rows each, and at most some two sequences each,
+// which a CTA takes in turn (a few microseconds each).
+constexpr int bal_ctas(int T, int S, int round, int most) {
+  int ctas = 1;
+  while (ctas < most && (ctas * round < T || 2 * ctas < (S < T ? S : T))) ctas *= 2;
+  return ctas;
+}
+static_assert(bal_ctas(64, 1, 64, 16) == 1 && bal_ctas(65, 1, 64, 16) == 2, "a round of rows each");
+static_assert(bal_ctas(8192, 1, 64, 16) == 16 && bal_ctas(8192, 1, 64, 8) == 8, "at most as many as the device places");
+static_assert(bal_ctas(64, 16, 64, 16) == 8 && bal_ctas(3, 900, 64, 16) == 2, "two sequences each");
+
 // Sequence bounds a block needs, checked: cu that decreases or leaves [0, T] is reported and counts as
 // no sequence at all.  Up to kBalSeqCache sequences' bounds are kept in shared memory, where looking a
 // token's sequence up does not wait for memory step by step.
@@ -217,7 +228,8 @@ __device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int h
       dot[r] *= inv;
       g[r] = wq * inv;
       if (there && ok && lane == 0) acc += 1.0 + (double)dot[r];
-      if (!there || !ok) skip |= (1u | (sum[r] < kBalSumMin ? 0x100u : 0u) | (sum[r] <= kBalSumMax ? 0u : 0x10000u)) << r;
+      const unsigned off = (sum[r] < kBalSumMin ? 0x100u : 0u) | (sum[r] <= kBalSumMax ? 0u : 0x10000u);
+      if (!there || !ok) skip |= (1u | off) << r;
       if (__any_sync(0xffffffffu, there && !ok)) rare |= 1u << r;
     }
     if (p.dscores) {

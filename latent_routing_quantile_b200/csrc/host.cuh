@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "../../include/lmoe.h"
@@ -86,16 +87,36 @@ cudaError_t ensure_smem_attr(K kern, int bytes, unsigned& done) {
   return e;
 }
 
-// Allows a kernel clusters of up to 16 CTAs (8 is the portable limit), once per device.
+// The largest cluster of `kern` (blocks of `threads`, no dynamic shared memory) that the current device
+// places: 16 CTAs, where it has that many SMs side by side, or 8, which every device has (a slice of a
+// partitioned one may not have 16).  `known` and `large` are the caller's own per-kernel flag words (one bit
+// per device): the device is asked once.
 template <typename K>
-cudaError_t allow_large_clusters(K kern, unsigned& done) {
+int largest_cluster(K kern, int threads, std::atomic<unsigned>& known, std::atomic<unsigned>& large) {
   int dev = 0;
   cudaGetDevice(&dev);
   const unsigned bit = 1u << (dev & 31);
-  if (done & bit) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) done |= bit;
-  return e;
+  if (!(known & bit)) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(threads);
+    cudaLaunchAttribute attr;
+    memset(&attr, 0, sizeof(attr));
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 16;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0)
+      large |= bit;
+    else
+      cudaGetLastError();  // not the launch's
+    known |= bit;
+  }
+  return (large & bit) ? 16 : 8;
 }
 
 // Launches `kern` with programmatic stream serialisation, so its blocks may be scheduled while

@@ -119,17 +119,14 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
   constexpr int kRound = kBalThreads / LANES * R;  // rows of one round of a block
   // One launch where a cluster streams the scores about as fast as the GPU gets through two launches
   // more (2048 x 256: 13.5 and 12.5 us on the GPU, 16 and 19.5 us with the host's launches; 512 x 64:
-  // 6.9 and 10.5; 4096 x 256: 19 and 13)
+  // 6.9 and 10.5; 4096 x 256: 19 and 13): 2^15 scores a CTA of the largest cluster
   const bool fits = (long long)p.S * p.E <= kBalHistInts;  // the cluster form's shared counters
-  if (fits && (long long)p.T * p.E <= (1ll << 19)) {
-    int ctas = 1;
-    // CTAs: a round of rows each, and at most some two sequences each, which a CTA takes in turn (a few
-    // microseconds each)
-    while (ctas < kBalMaxCluster && (ctas * kRound < p.T || 2 * ctas < std::min(p.S, p.T))) ctas *= 2;
+  auto kern = balance_cluster_kernel<NJ, VEC, R, LANES>;
+  static std::atomic<unsigned> known{0}, large{0};
+  const int most = fits ? largest_cluster(kern, kBalThreads, known, large) : 0;
+  if ((long long)p.T * p.E <= (long long)most << 15) {
+    const int ctas = bal_ctas(p.T, p.S, kRound, most);
     p.chunk = (p.T + ctas - 1) / ctas;
-    static unsigned done = 0;
-    auto kern = balance_cluster_kernel<NJ, VEC, R, LANES>;
-    CK(allow_large_clusters(kern, done));
     CK(launch_k(kern, dim3(ctas), dim3(kBalThreads), 0, st, ctas, p));
     return LMOE_OK;
   }

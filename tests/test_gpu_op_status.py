@@ -79,3 +79,33 @@ def test_wrong_words_are_refused():
         with pytest.raises(lq.LmoeError):
             lq.mx4_quant(x, status=bad)
     assert lq.op_status() == 0
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """What a kernel asks the device once (its largest cluster, its shared memory) may be asked under a capture:
+    the first calls of a process, in one graph, for every form."""
+    import os
+    import subprocess
+    import sys
+    code = """if True:
+        import torch, latent_routing_quantile_b200 as lq
+        cases = [(50, 64, 4), (700, 256, 6), (9000, 256, 6), (300, 33, 2), (200, 896, 16), (2048, 256, 6), (4000, 64, 4)]
+        g = torch.Generator(device="cuda").manual_seed(1)
+        s = [torch.rand(T, E, generator=g, device="cuda") for T, E, k in cases]
+        i = [v.topk(c[2], dim=1).indices.int() for v, c in zip(s, cases)]
+        x, w = torch.randn(70, 4128, generator=g, device="cuda"), torch.randn(256, 4128, generator=g, device="cuda")
+        mine = torch.zeros(1, dtype=torch.int32, device="cuda")
+        run = lambda: [lq.balance_loss(a, b, 0.1, status=mine) for a, b in zip(s, i)] + \\
+            [dict(c=lq.mx4_gemm(lq.mx4_quant(x, status=mine), lq.mx4_quant(w, status=mine), status=mine))]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        graph.replay()
+        for a, b in zip(out, run()):
+            assert all(torch.equal(a[n], b[n]) for n in b)
+        assert int(mine) == 0
+        print("same")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
