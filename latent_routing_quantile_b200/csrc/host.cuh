@@ -150,10 +150,11 @@ cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// lmoe_balance_loss with S' from a device word where that is more than 0 (total: null for none).
+// lmoe_balance_loss with S' from a device word where that is more than 0 (total: null for none), which adds
+// the kernels it launched to *launches (null: not counted).
 int balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_t E, int32_t k, const int32_t* cu_seqlens,
                  int32_t S, const int32_t* total, float coef, int32_t* counts, float* loss, float* dscores,
-                 void* scratch, uint32_t* status, void* stream);
+                 void* scratch, uint32_t* status, void* stream, long long* launches);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -1521,9 +1521,8 @@ int backward_bf16(lmoe_handle* h, const lmoe_weights* w, const void* x, const vo
   }
   if (h->bal_on) {  // the balance loss of this step's scores and choice, and its gradient in the scores
     int rc = balance_loss(h->s, h->idx, T, c.E, c.k, h->bal_cu, h->bal_S, h->bal_total, h->bal_coef, h->bal_counts,
-                          h->bal_loss, h->bal_ds, h->bal_scratch, h->status, st);
+                          h->bal_loss, h->bal_ds, h->bal_scratch, h->status, st, &h->launches);
     if (rc) return rc;
-    h->launches += 1;
   }
   // combine and gates: dL/do of every pair, dL/dlogit
   CK(launch_k(combine_bwd_kernel, dim3((T + 7) / 8), dim3(256), 0, st, 1, (const bf16*)b->dz, (const bf16*)h->o,

@@ -115,7 +115,7 @@ Mx4Plan plan_mx4(int M, int N, int nkb, int groups, bool ragged, int sms) {
 
 // The balance loss in one launch (a cluster) or two (see balance.cuh).
 template <int NJ, int VEC, int R, int LANES>
-int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
+int launch_balance(BalanceParams& p, int sms, cudaStream_t st, long long* launches) {
   constexpr int kRound = kBalThreads / LANES * R;  // rows of one round of a block
   // One launch where a cluster streams the scores about as fast as the GPU gets through two launches
   // more (2048 x 256: 13.5 and 12.5 us on the GPU, 16 and 19.5 us with the host's launches; 512 x 64:
@@ -128,6 +128,7 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
     const int ctas = bal_ctas(p.T, p.S, kRound, most);
     p.chunk = (p.T + ctas - 1) / ctas;
     CK(launch_k(kern, dim3(ctas), dim3(kBalThreads), 0, st, ctas, p));
+    if (launches) *launches += 1;
     return LMOE_OK;
   }
   CK(cudaMemsetAsync(p.counts, 0, (size_t)p.S * p.E * sizeof(int32_t), st));
@@ -140,6 +141,7 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
   const int blocks = std::min(2 * sms, kBalMaxBlocks);
   p.chunk = std::max(std::min(kRound, per_seq), (p.T + blocks - 1) / blocks);
   CK(launch_k(balance_kernel<NJ, VEC, R, LANES>, dim3((p.T + p.chunk - 1) / p.chunk), dim3(kBalThreads), 0, st, 1, p));
+  if (launches) *launches += 2;
   return LMOE_OK;
 }
 
@@ -147,7 +149,8 @@ int launch_balance(BalanceParams& p, int sms, cudaStream_t st) {
 
 int lmoe::balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_t E, int32_t k,
                        const int32_t* cu_seqlens, int32_t S, const int32_t* total, float coef, int32_t* counts,
-                       float* loss, float* dscores, void* scratch, uint32_t* status, void* stream) {
+                       float* loss, float* dscores, void* scratch, uint32_t* status, void* stream,
+                       long long* launches) {
   if (T < 0 || E <= 0 || k <= 0 || k > E || S <= 0 || (!cu_seqlens && S != 1) || !(coef == coef)) return LMOE_EINVAL;
   if (E > kBalMaxE || k > 32 || S > kBalMaxSeqs || (long long)T * k > (1ll << 30)) return LMOE_EUNSUPPORTED;
   if (!words(counts) || !words(loss) || !words(status) || !scratch || ((uintptr_t)scratch & 15)) return LMOE_EINVAL;
@@ -183,16 +186,16 @@ int lmoe::balance_loss(const float* scores, const int32_t* idx, int32_t T, int32
   // sets of rows in flight: what fits 64 registers; rows of few experts share a warp (262144 x 8 19 us
   // against 39 with a row a warp, 65536 x 64 15 against 19)
   if (vec) {
-    if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st);
-    if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st);
-    if (E <= 128) return launch_balance<1, 4, 4, 32>(p, sms, st);
-    if (E <= 256) return launch_balance<2, 4, 4, 32>(p, sms, st);
-    if (E <= 512) return launch_balance<4, 4, 2, 32>(p, sms, st);
-    return launch_balance<8, 4, 2, 32>(p, sms, st);
+    if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st, launches);
+    if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st, launches);
+    if (E <= 128) return launch_balance<1, 4, 4, 32>(p, sms, st, launches);
+    if (E <= 256) return launch_balance<2, 4, 4, 32>(p, sms, st, launches);
+    if (E <= 512) return launch_balance<4, 4, 2, 32>(p, sms, st, launches);
+    return launch_balance<8, 4, 2, 32>(p, sms, st, launches);
   }
-  if (E <= 64) return launch_balance<2, 1, 4, 32>(p, sms, st);
-  if (E <= 256) return launch_balance<8, 1, 4, 32>(p, sms, st);
-  return launch_balance<32, 1, 1, 32>(p, sms, st);
+  if (E <= 64) return launch_balance<2, 1, 4, 32>(p, sms, st, launches);
+  if (E <= 256) return launch_balance<8, 1, 4, 32>(p, sms, st, launches);
+  return launch_balance<32, 1, 1, 32>(p, sms, st, launches);
 }
 
 extern "C" {
@@ -380,7 +383,7 @@ int lmoe_balance_loss(const float* scores, const int32_t* idx, int32_t T, int32_
                       const int32_t* cu_seqlens, int32_t S, float coef, int32_t* counts, float* loss, float* dscores,
                       void* scratch, uint32_t* status, void* stream) {
   return balance_loss(scores, idx, T, E, k, cu_seqlens, S, nullptr, coef, counts, loss, dscores, scratch, status,
-                      stream);
+                      stream, nullptr);
 }
 
 }  // extern "C"

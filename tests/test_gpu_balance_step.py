@@ -141,3 +141,24 @@ def test_data_parallel_step_of_one_rank_on_a_named_stream(step):
                 assert torch.allclose(g[n], ref[n], rtol=1e-4, atol=1e-4 * float(ref[n].abs().max())), n
     finally:
         dist.destroy_process_group()
+
+
+@pytest.mark.parametrize("T,kernels", [(256, 1), (8300, 2)])
+def test_launch_count_of_a_step(T, kernels):
+    """The loss is one kernel up to 2^19 scores and two above; two more sum the offsets' gradient.  Eager,
+    captured and replayed steps count alike."""
+    step = Step(T=T)
+    grads = step.run()
+
+    def counts():
+        out = []
+        for _ in range(4):
+            before = step.layer.launches()
+            step.run(grads=grads)
+            out.append(step.layer.launches() - before)
+        return out
+
+    without = counts()
+    step.layer.set_balance(1.0)
+    assert counts() == [n + kernels + 2 for n in without]
+    step.layer.close()
