@@ -329,30 +329,6 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
   return d;
 }
 
-// ---- scale atoms of the block-scaled products (8-bit and 4-bit)
-// Shared-memory descriptor of a 32-row x 16-byte matrix stored row after row, without swizzle:
-// core matrices of 8 rows x 16 bytes, 128 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(128u >> 4) << 16;
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  return d;
-}
-// Copies a 512-byte scale atom from shared memory into TMEM columns [taddr, taddr + 4) of all four
-// lane quarters (ordered with this thread's later MMAs).
-__device__ __forceinline__ void tc_cp_atom(uint32_t taddr, uint32_t saddr) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(smem_desc_rows16(saddr)));
-}
-// Bulk copy (no tensor map) of `bytes` from global to shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // 16 bytes from global memory through the non-coherent path (data no kernel of the launch writes).
 __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   uint4 v;
