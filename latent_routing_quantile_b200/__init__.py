@@ -306,8 +306,9 @@ class Layer:
     def balance(self, stream=None):
         """(loss [1], counts [S, E]) of the last training step since set_balance; zeros before the first."""
         S = 1 if self._balance is None else self._balance[1]
-        loss = torch.empty(1, dtype=torch.float32, device="cuda")
-        counts = torch.empty((S, self.cfg.E), dtype=torch.int32, device="cuda")
+        with _current(stream):  # the results belong to the stream that writes them
+            loss = torch.empty(1, dtype=torch.float32, device="cuda")
+            counts = torch.empty((S, self.cfg.E), dtype=torch.int32, device="cuda")
         _check(lib().lmoe_get_balance(self.handle, _ptr(loss), _ptr(counts), _stream(stream)), "lmoe_get_balance")
         return loss, counts
 

@@ -162,3 +162,19 @@ def test_launch_count_of_a_step(T, kernels):
     step.layer.set_balance(1.0)
     assert counts() == [n + kernels + 2 for n in without]
     step.layer.close()
+
+
+def test_results_on_a_named_stream_belong_to_it(step):
+    """balance(stream) writes into memory of that stream's: a block that the current stream has let go of may
+    still be read there by work that is queued."""
+    step.layer.set_balance(1.0)
+    step.run()
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), None):
+        loss, counts = step.layer.balance(stream=stream)
+        torch.cuda.synchronize()
+        assert int(counts.sum()) == 4 * 256 and float(loss) > 0
+        for t in (loss, counts):
+            owner = [s["stream"] for s in torch.cuda.memory_snapshot()
+                     if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+            assert owner == [0 if stream is None else stream.cuda_stream]
