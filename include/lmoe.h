@@ -411,10 +411,10 @@ int lmoe_mx4_gemm(const uint8_t *a_elems, const uint8_t *a_scales, const uint8_t
  * no part and gets a zero gradient; so does a token whose scores sum to zero.  Scores of any finite
  * size count alike, down to the smallest; a gradient past fp32's range (it grows as 1 / sum_j s_tj) is
  * held at its largest value.  A NaN or infinite score makes the loss and its token's gradient NaN and
- * sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index other than -1 outside [0, E) is not counted, and it, or cu_seqlens that decrease or leave [0, T],
- * sets LMOE_STATUS_BAD_INDEX (the bits are ORed in, never cleared).
- * E at most 1024, k at most 32, S at most 2^24, T k at most 2^30.  scratch is lmoe_balance_scratch_bytes of device memory, 16-byte
- * aligned, the call's own until it has run.  Sums are taken in a fixed order: the same call gives
+ * sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index other than -1 outside [0, E) is not
+ * counted, and it, or cu_seqlens that decrease or leave [0, T], sets LMOE_STATUS_BAD_INDEX (the bits are
+ * ORed in, never cleared).  E at most 1024, k at most 32, S at most 2^24, T k at most 2^30.  scratch is
+ * lmoe_balance_scratch_bytes of device memory, 16-byte aligned, the call's own until it has run.  Sums are taken in a fixed order: the same call gives
  * the same bits every time. */
 int lmoe_balance_scratch_bytes(size_t *bytes);
 int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_t E, int32_t k,

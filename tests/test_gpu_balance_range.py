@@ -162,6 +162,27 @@ def test_loss_of_tens_of_millions_of_tokens(equal):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("T,E,k", [(640, 64, 4), (512, 256, 6), (9000, 64, 4), (1792, 896, 16), (660, 33, 3)])
+def test_next_to_balance(T, E, k):
+    """Choices in turn with a few swaps: |f - 1| is some 1e-2 and less, and the gradient is held to that size, not
+    to that of f and D (which an fp32 f - D would miss, as the last lines show)."""
+    s, _ = inputs(T, E, k, 9 * E)
+    idx = (torch.arange(T * k) % E).view(T, k).int()
+    for t in range(0, T, T // 5):
+        idx[t, 0] = idx[t, 1]
+    out = lq.balance_loss(s.cuda(), idx.cuda(), 0.25)
+    cnt, loss, slack, g, scale = reference(s, idx, [0, T], 0.25)
+    assert np.array_equal(out["counts"].cpu().numpy(), cnt)
+    assert abs(float(out["loss"]) - loss) <= 16 * U * loss + 84 * U * slack
+    tol = 136 * U * scale
+    assert (np.abs(out["dscores"].cpu().double().numpy() - g) <= tol).all()
+    f = (cnt[0] * (E / (k * T))).astype(np.float32)
+    R = s.numpy().sum(1, dtype=np.float32, keepdims=True)
+    D = (s.numpy() / R) @ f
+    cancelled = np.float32(0.25) / T * (f - D[:, None]) / R
+    assert (np.abs(cancelled - g) > tol).any()
+
+
 def test_no_gradient_is_returned_that_was_not_made():
     """grad=False with the buffers of an earlier call: its gradient is left alone and not handed on."""
     s, idx = inputs(50, 64, 4, 41)
