@@ -44,6 +44,10 @@ METRIC = "LatentMoE layer fwd tokens/s on 1 B200; % BF16 tensor peak; router/per
 UNIT = "tokens/s"
 BETA = 0.01
 EXPERT_FORMATS = {"bf16": 0, "mxfp8": 1, "mxfp4": 4}  # the binding's EXPERTS_* values
+# bytes of an operand value of the routed experts (a scale byte for 32 values), and the tensor rate in
+# bf16's (the dense fp8 rate is twice bf16's, the 4-bit one four times)
+EXPERT_BYTES = {1: 1 + 1 / 32, 4: 0.5 + 1 / 32}
+EXPERT_RATE = {0: 1, 1: 2, 4: 4}
 FLUSH_BYTES = 256 << 20
 FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustained": 1400.0}
 
@@ -76,10 +80,12 @@ def csrc_digest(files=None) -> str:
     return h.hexdigest()[:16]
 
 
-def stage_work(shape, T):
-    """Algorithmic FLOPs and HBM bytes of one launch of each stage on T tokens (bf16 storage)."""
+def stage_work(shape, T, experts=0):
+    """Algorithmic FLOPs and HBM bytes of one launch of each stage on T tokens (bf16 storage; the routed
+    experts' rows, weights and activations in the format `experts`)."""
     d, l, E, k, h, hs = shape.d, shape.l, shape.E, shape.k, shape.h, shape.hs
     w = 2 if shape.dtype == "bf16" else 4
+    we = EXPERT_BYTES.get(experts, w)
     TK = T * k
     nblk = (T + 127) // 128
     return {
@@ -92,11 +98,11 @@ def stage_work(shape, T):
         "plan": (0, 3 * 4 * nblk * E),
         # compulsory: each h row read once (its k copies come from L2), A_perm written, idx read,
         # perm and inv written
-        "gather": (0, T * w * l + TK * (w * l + 12)),
+        "gather": (0, T * w * l + TK * (we * l + 12)),
         "hist": (0, 2 * T * E + 8 * E * 4096),
         "shared_swiglu": (4 * T * d * hs, T * w * d + 2 * hs * d * w + T * w * hs),
-        "expert_swiglu": (4 * TK * l * h, TK * w * l + 2 * E * h * l * w + TK * w * h),
-        "expert_down": (2 * TK * h * l, TK * w * h + E * l * h * w + TK * w * l),
+        "expert_swiglu": (4 * TK * l * h, TK * we * l + 2 * E * h * l * we + TK * we * h),
+        "expert_down": (2 * TK * h * l, TK * we * h + E * l * h * we + TK * w * l),
         "combine": (0, TK * (w * l + 8) + T * w * l),
         "up_proj": (2 * T * d * (l + hs), T * w * (l + hs) + d * (l + hs) * w + T * w * d),
         # the update counts the last forward's pending bins (2 B per score) itself
@@ -269,7 +275,7 @@ def measure(shape, args, rank, world, local_rank, e2e=True, experts=0):
         return None, launches
 
     peaks, peak_src = load_peaks()
-    work = stage_work(shape, T)
+    work = stage_work(shape, T, experts)
     per_launch = {n: stage_ms[n] / max(1, nfwd) for n in stage_ms}
     # with l <= 256 and E <= 256 the library runs rms, down_proj and router as one kernel
     # (norm_down_router); their own markers then bracket no work, only event overhead
@@ -287,7 +293,8 @@ def measure(shape, args, rank, world, local_rank, e2e=True, experts=0):
         t_s = t / 1e3
         if t_s <= 0:
             continue
-        t_tensor = fl / (peaks["bf16_tflops"] * 1e12) if fl else 0.0
+        rate = EXPERT_RATE[experts] if n.startswith("expert_") else 1
+        t_tensor = fl / (peaks["bf16_tflops"] * rate * 1e12) if fl else 0.0
         t_hbm = by / (peaks["hbm_gbs"] * 1e9)
         bound = "tensor" if t_tensor >= t_hbm else "hbm"
         kernels[n] = {"ms": round(t, 5), "share": round(t / step_stage_ms, 4), "bound": bound,
@@ -303,9 +310,7 @@ def measure(shape, args, rank, world, local_rank, e2e=True, experts=0):
     rpc_ms = sum(per_launch[n] for n in rpc)
     ex_flops = work["expert_swiglu"][0] + work["expert_down"][0]
     ex_ms = per_launch["expert_swiglu"] + per_launch["expert_down"]
-    # 8-bit experts run at twice the bf16 tensor rate (the dense fp8 rate is twice bf16's), 4-bit ones at
-    # four times
-    ex_peak = peaks["bf16_tflops"] * {0: 1, 1: 2, 4: 4}[experts]
+    ex_peak = peaks["bf16_tflops"] * EXPERT_RATE[experts]
     summary = {
         "workload": shape.name, "T": T, "ms_per_step": round(ms_max, 5),
         "value": round(T * world / (ms_max / 1e3), 1),
