@@ -302,6 +302,8 @@ class Layer:
         if total is not None:
             _dev(total, torch.int32, (1,), "total")
         _check(lib().lmoe_set_balance_total(self.handle, _ptr(total), _stream(stream)), "lmoe_set_balance_total")
+        if total is not None and stream is not None:
+            total.record_stream(stream)
 
     def balance(self, stream=None):
         """(loss [1], counts [S, E]) of the last training step since set_balance; zeros before the first."""
@@ -486,9 +488,11 @@ def dp_train_step(layer, x, dy, weights, beta=None, literal=False, sign_rule=Fal
         if total is not None:
             dist.all_reduce(total, group=group)
             layer.set_balance_total(total, stream)
-        y, g = layer.forward_backward(x, dy, weights, record_stats=True, grads=grads, stream=stream)
-        if total is not None:
-            layer.set_balance_total(None, stream)
+        try:
+            y, g = layer.forward_backward(x, dy, weights, record_stats=True, grads=grads, stream=stream)
+        finally:
+            if total is not None:
+                layer.set_balance_total(None, stream)
         for name, t in g.items():
             if name != "x":
                 dist.all_reduce(t, group=group)

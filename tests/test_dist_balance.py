@@ -120,6 +120,21 @@ def test_no_exchange_without_a_balance_loss():
     assert layer.balance_sequences(9) is None
 
 
+def test_a_refused_step_leaves_the_layer_to_its_own_sequences(monkeypatch):
+    """The other ranks' sequences are one step's: a step that raises does not leave them to the next."""
+    layer = BalanceLayer(None, [0, 4])
+
+    def refused(*args, **kw):
+        assert layer.total == 1
+        raise lq.LmoeError("refused")
+
+    monkeypatch.setattr(dist, "all_reduce", lambda t, group=None: None)
+    monkeypatch.setattr(layer, "forward_backward", refused)
+    with pytest.raises(lq.LmoeError, match="refused"):
+        lq.dp_train_step(layer, torch.zeros(4, 8), None, None)
+    assert layer.total == 0
+
+
 def test_collectives_follow_the_named_stream(monkeypatch):
     """On a stream that the caller names, every collective and every tensor made for one is issued with that
     stream current: the sums would otherwise not wait for the step that writes what they sum."""
