@@ -74,6 +74,11 @@ struct BalSeqs {
     }
     return lo;
   }
+  // The sequence after q to look at: a run of empty ones, which may be millions, is stepped over at once.
+  __device__ __forceinline__ int next(int q) const {
+    ++q;
+    return q < S && begin(q) == begin(q + 1) ? at(begin(q)) : q;
+  }
 };
 struct BalSeqSmem {
   int cu[kBalSeqCache + 1];
@@ -278,7 +283,7 @@ __device__ __forceinline__ double bal_pass(const BalanceParams& p, const BalSeqs
     for (long long i = (long long)t0 * p.E + threadIdx.x; i < a1; i += kBalThreads) p.dscores[i] = 0.f;
     for (long long i = b0 + threadIdx.x; i < b1; i += kBalThreads) p.dscores[i] = 0.f;
   }
-  for (int q = max(sq.at(t0), 0); q < sq.S; ++q) {
+  for (int q = max(sq.at(t0), 0); q < sq.S; q = sq.next(q)) {
     const int b = sq.begin(q), e = sq.begin(q + 1);
     if (b >= t1) break;
     if (max(b, t0) >= min(e, t1)) continue;
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const Balanc
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
   const int copies = bal_copies(p.E);
-  for (int q = max(sq.at(t0), 0); q < sq.S; ++q) {
+  for (int q = max(sq.at(t0), 0); q < sq.S; q = sq.next(q)) {
     const int b = sq.begin(q), lo = max(t0, b), hi = min(t1, sq.begin(q + 1));
     if (b >= t1) break;
     if (lo >= hi) continue;
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_cluster_kernel(const B
   const BalSeqs sq = bal_seqs(p, seqs);  // ends with a barrier
   const int t0 = min(p.T, rank * p.chunk), t1 = min(p.T, t0 + p.chunk);
   if (t0 < t1)
-    for (int q = max(sq.at(t0), 0); q < sq.S; ++q) {
+    for (int q = max(sq.at(t0), 0); q < sq.S; q = sq.next(q)) {
       const int b = sq.begin(q), lo = max(t0, b), hi = min(t1, sq.begin(q + 1));
       if (b >= t1) break;
       if (lo < hi) bal_count(p, lo, hi, hist + q * p.E * copies, copies);

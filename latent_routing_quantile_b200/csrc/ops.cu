@@ -183,9 +183,8 @@ int lmoe::balance_loss(const float* scores, const int32_t* idx, int32_t T, int32
   p.partial = reinterpret_cast<double*>(static_cast<char*>(scratch) + 256);
   p.status = status;
   const bool vec = E % 4 == 0 && (((uintptr_t)scores | (uintptr_t)dscores) & 15) == 0;
-  // sets of rows in flight: what fits the 64 registers that two blocks an SM leave a thread (with more than
-  // 512 experts one of them is spilled); rows of few experts share a warp (262144 x 8 19 us against 39 with
-  // a row a warp, 65536 x 64 15 against 19)
+  // sets of rows in flight: what fits the 64 registers that two blocks an SM leave a thread; rows of few
+  // experts share a warp (262144 x 8 19 us against 39 with a row a warp, 65536 x 64 15 against 19)
   if (vec) {
     if (E <= 32) return launch_balance<1, 4, 4, 8>(p, sms, st, launches);
     if (E <= 64) return launch_balance<1, 4, 4, 16>(p, sms, st, launches);

@@ -183,6 +183,45 @@ def test_next_to_balance(T, E, k):
     assert (np.abs(cancelled - g) > tol).any()
 
 
+@pytest.mark.parametrize("where", ["before", "between", "behind"])
+def test_runs_of_empty_sequences_are_stepped_over(where):
+    """A million bounds alike: the results of the bounds without them, and no walk through each (which took a
+    block 88 ms)."""
+    T, E, k, n = 300, 64, 4, 1 << 20
+    s, idx = inputs(T, E, k, 55)
+    sd, id_ = s.cuda(), idx.cuda()
+    short, at = [20, 100, 250], ["before", "between", "behind"].index(where)
+    cu = short[:at] + [short[at]] * (n + 1) + short[at + 1:]
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    ref = lq.balance_loss(sd, id_, 0.25, cu_seqlens=torch.tensor(short, dtype=torch.int32, device="cuda"))
+    lq.balance_loss(sd, id_, 0.25, cu_seqlens=cud)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    out = lq.balance_loss(sd, id_, 0.25, cu_seqlens=cud)
+    b.record()
+    torch.cuda.synchronize()
+    assert a.elapsed_time(b) < 20  # the bounds' checks, and 268 MB of counts set to zero
+    full = out["counts"].sum(dim=1).nonzero().flatten()
+    assert torch.equal(out["counts"][full], ref["counts"]) and len(full) == 2
+    assert abs(float(out["loss"]) - float(ref["loss"])) <= 16 * U * float(ref["loss"])
+    check({"counts": ref["counts"], "loss": out["loss"], "dscores": out["dscores"]}, s, idx, short, 0.25)
+
+
+@pytest.mark.parametrize("cu", [[0, 0, 0, 5, 5, 5, 9, 9, 9], [3, 3, 4, 4, 4, 4], [7, 7, 7], [0, 0, 300, 300], [300, 300],
+                                [0, 0, 0, 0], [5, 5, 290, 290, 290, 300]])
+@pytest.mark.parametrize("E", [64, 1023])
+def test_empty_sequences_anywhere(cu, E):
+    T, k = 300, 4
+    s, idx = inputs(T, E, k, 56)
+    check(lq.balance_loss(s.cuda(), idx.cuda(), 0.25, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda")), s,
+          idx, cu, 0.25)
+    # the same in the form of two launches: the tokens behind are in no sequence
+    T2 = (1 << 19) // E + 500
+    s, idx = inputs(T2, E, k, 57)
+    check(lq.balance_loss(s.cuda(), idx.cuda(), 0.25, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda")), s,
+          idx, cu, 0.25)
+
+
 def test_no_gradient_is_returned_that_was_not_made():
     """grad=False with the buffers of an earlier call: its gradient is left alone and not handed on."""
     s, idx = inputs(50, 64, 4, 41)
