@@ -414,8 +414,8 @@ int lmoe_mx4_gemm(const uint8_t *a_elems, const uint8_t *a_scales, const uint8_t
  * sets LMOE_STATUS_NAN_SCORE in *status_dev; an expert index other than -1 outside [0, E) is not
  * counted, and it, or cu_seqlens that decrease or leave [0, T], sets LMOE_STATUS_BAD_INDEX (the bits are
  * ORed in, never cleared).  E at most 1024, k at most 32, S at most 2^24, T k at most 2^30.  scratch is
- * lmoe_balance_scratch_bytes of device memory, 16-byte aligned, the call's own until it has run.  Sums are taken in a fixed order: the same call gives
- * the same bits every time. */
+ * lmoe_balance_scratch_bytes of device memory, 16-byte aligned, the call's own until it has run.  Sums
+ * are taken in a fixed order: the same call gives the same bits every time. */
 int lmoe_balance_scratch_bytes(size_t *bytes);
 int lmoe_balance_loss(const float *scores, const int32_t *idx, int32_t T, int32_t E, int32_t k,
                       const int32_t *cu_seqlens, int32_t S, float coef, int32_t *counts, float *loss, float *dscores,

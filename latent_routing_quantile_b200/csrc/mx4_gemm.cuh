@@ -21,11 +21,12 @@
 // ring itself (they released the stage before it was loaded again).
 //
 // Measured: 16384 x 8192 x 7168 with the SwiGLU epilogue 356 us, 5.4 PFLOP/s (the MMAs alone 290 us, the
-// loads alone 275); sustained, at the power cap's clock, 424 us.  Together they are held by shared
-// memory: a k-block of a 128 x 256 tile writes 51 KB and reads 48 KB of it, 774 cycles at 128 bytes a
-// cycle, of the 890 that it takes.  The wide layer's gate and linear projections (262144 rows over 896
-// experts, 1024 x 2048) 344 us: MMAs alone 220, a quarter of them for the rows that fill up an expert's
-// last tile, loads alone 224.
+// loads alone 275); sustained, at the power cap's clock, 424 us.  The tensor pipe is the busiest unit, 73% of
+// the cycles (a k-block of a 128 x 256 tile takes 702 of them, its MMAs 512), L2 at 62%, the banks of
+// shared memory at 33% for reads and 28% for writes.  The wide layer's gate and linear projections (262144
+// rows over 896 experts, 1024 x 2048) 344 us: MMAs alone 220, a quarter of them for the rows that fill up an
+// expert's last tile, loads alone 224; a quarter of its tokens and experts keeps the tensor pipe busy for
+// 52% of the cycles and DRAM for 53%.
 #pragma once
 
 #include "mx4.cuh"
