@@ -178,3 +178,27 @@ def test_results_on_a_named_stream_belong_to_it(step):
             owner = [s["stream"] for s in torch.cuda.memory_snapshot()
                      if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
             assert owner == [0 if stream is None else stream.cuda_stream]
+
+
+def test_replayed_steps_of_large_batches_take_their_own_scores():
+    """Above 2^19 scores (zeroed counts, counting, the pass: three nodes of the replayed backward), with inputs
+    that change between the replays: loss and counts of the step's own scores and choice."""
+    import oracle.balance as ob
+    step = Step(T=8300)
+    cu = [0, 1000, 1000, 5000, 8200]
+    step.layer.set_balance(3.0, bounds(*cu))
+    grads = step.run()
+    x = step.x.clone()
+    for i in range(4):
+        step.x.copy_(x.roll(7 * i, 0))
+        step.run(grads=grads)
+        loss, counts = step.layer.balance()
+        r = step.layer.routing()
+        s, idx = r["scores"].double().cpu().numpy(), r["idx"].cpu().numpy()
+        cnt = ob.counts(idx, 64, cu)
+        assert np.array_equal(counts.cpu().numpy(), cnt)
+        ref = ob.loss(s, cnt, 4, cu, 3.0)
+        # each token's D to 84 u of its size and of 1, D near 1 here: 256 u of the mean
+        assert abs(float(loss) - ref) <= 256 * 2.0 ** -24 * ref
+    assert step.layer.status() == 0
+    step.layer.close()
