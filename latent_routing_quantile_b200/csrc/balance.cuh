@@ -65,9 +65,9 @@ struct BalSeqs {
   const int* cu;   // shared or global
   int S, filled;   // sequences; S'
   __device__ __forceinline__ int begin(int q) const { return cu[q]; }
-  // The last sequence that begins at or before token t (-1: none does).
-  __device__ __forceinline__ int at(int t) const {
-    int lo = -1, hi = S;
+  // The last sequence behind lo that begins at or before token t (lo: none does).
+  __device__ __forceinline__ int at(int t, int lo = -1) const {
+    int hi = S;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (begin(mid) <= t) lo = mid; else hi = mid;
@@ -75,9 +75,10 @@ struct BalSeqs {
     return lo;
   }
   // The sequence after q to look at: a run of empty ones, which may be millions, is stepped over at once.
+  // Always past q, also where the caller's bounds change under the kernel: its loops end.
   __device__ __forceinline__ int next(int q) const {
     ++q;
-    return q < S && begin(q) == begin(q + 1) ? at(begin(q)) : q;
+    return q < S && begin(q) == begin(q + 1) ? at(begin(q), q) : q;
   }
 };
 struct BalSeqSmem {
