@@ -131,28 +131,34 @@ __device__ __forceinline__ void bal_count(const BalanceParams& p, int lo, int hi
 constexpr float kBalSumMin = 0x1p-60f, kBalSumMax = 0x1p60f;
 
 // One row by itself, LANES lanes a row (`there` is false for lanes without one).  f: shared, f - 1 and,
-// kBalMaxE further, f.  c scales the scores: a power of two where they are so small that 1 / R overflows or
-// so large that R does, which D does not see and the gradient's 1 / R gives back.  D < 1/2 is summed as
-// it is, D above as D - 1.  A gradient past fp32 saturates at its largest value; a row of zeros has no
+// kBalMaxE further, f.  Scores so small that 1 / R overflows or so large that R does are taken again times c, a
+// power of two, which D does not see and the gradient's 1 / R gives back.  D < 1/2 is summed as it is, D
+// above as D - 1.  A gradient past fp32 saturates at its largest value; a row of zeros has no
 // probabilities: it adds nothing and gets no gradient.  Returns D in the row's first lane.  A batch of
 // such rows alone takes 50 us at 16384 x 896 for 29 of ordinary ones, 16.5 us at 8192 x 256 for 12.5.
 template <int LANES>
 __device__ __forceinline__ double bal_row_alone(const float* srow, float* drow, int E, const float* f, float wq,
-                                                float c, bool there, bool& nan) {
+                                                bool there, bool& nan) {
   const int lane = threadIdx.x & (LANES - 1), end = there ? E : 0;
-  float sum = 0.f, dot = 0.f, whole = 0.f;
+  float c = 1.f, sum, dot, whole;
+  for (bool again = false;; again = true) {
+    sum = dot = whole = 0.f;
 #pragma unroll 4
-  for (int e = lane; e < end; e += LANES) {
-    const float v = srow[e] * c;
-    sum += v;
-    dot = fmaf(v, f[e], dot);
-    whole = fmaf(v, f[kBalMaxE + e], whole);
-  }
+    for (int e = lane; e < end; e += LANES) {
+      const float v = srow[e] * c;
+      sum += v;
+      dot = fmaf(v, f[e], dot);
+      whole = fmaf(v, f[kBalMaxE + e], whole);
+    }
 #pragma unroll
-  for (int off = LANES / 2; off; off >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    whole += __shfl_xor_sync(0xffffffffu, whole, off);
+    for (int off = LANES / 2; off; off >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      whole += __shfl_xor_sync(0xffffffffu, whole, off);
+    }
+    const bool inside = sum >= kBalSumMin && sum <= kBalSumMax;
+    if (again || !__any_sync(0xffffffffu, there && !inside)) break;
+    if (!inside) c = sum < kBalSumMin ? 0x1p64f : 0x1p-64f;
   }
   nan |= !(fabsf(sum) <= 3.4028234e38f);
   const bool some = sum != 0.f, low = dot < -0.5f * sum;
@@ -178,7 +184,9 @@ template <int NJ, int VEC, int R, int LANES>
 __device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
   constexpr int kSide = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LANES - 1), side = (threadIdx.x & 31) / LANES;
-  double acc = 0;  // a lane's rows may be thousands, and 1 + (D - 1) drops the low bits of D - 1 in 32 bits
+  // D is summed as what the rows' differ from 1 by and their number, in 64 bits: a lane's rows may be thousands
+  double acc = 0, alone = 0;
+  int n = 0;
   for (int t0 = lo + warp * R * kSide + side; t0 - side < hi; t0 += kBalThreads / 32 * R * kSide) {
     float s[R][NJ * VEC], sum[R], dot[R];
 #pragma unroll
@@ -223,9 +231,8 @@ __device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int h
         dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], off);
       }
     float g[R];
-    // sets in which this lane's row is not there or left to bal_row_alone (bits 0 on), its sum too small
-    // (8 on) or too large or no number (16 on); sets in which some lane's row is left
-    unsigned skip = 0, rare = 0;
+    unsigned skip = 0, left = 0;  // sets in which this lane's row is not there or left to bal_row_alone; is left
+    float part = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const bool there = t0 + r * kSide < hi;
@@ -233,11 +240,12 @@ __device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int h
       const float inv = 1.f / sum[r];
       dot[r] *= inv;
       g[r] = wq * inv;
-      if (there && ok && lane == 0) acc += 1.0 + (double)dot[r];
-      const unsigned off = (sum[r] < kBalSumMin ? 0x100u : 0u) | (sum[r] <= kBalSumMax ? 0u : 0x10000u);
-      if (!there || !ok) skip |= (1u | off) << r;
-      if (__any_sync(0xffffffffu, there && !ok)) rare |= 1u << r;
+      if (there && ok) part += dot[r];
+      else skip |= 1u << r;
+      if (there && !ok) left |= 1u << r;
     }
+    acc += (double)part;
+    n += R - __popc(skip);
     if (p.dscores) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -256,17 +264,15 @@ __device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int h
         }
       }
     }
+    const unsigned rare = __reduce_or_sync(0xffffffffu, left);
 #pragma unroll 1
     for (int r = 0; rare >> r; ++r) {
       if (!((rare >> r) & 1)) continue;
-      const int t = t0 + r * kSide;
-      const long long at = (long long)t * p.E;
-      acc += bal_row_alone<LANES>(p.scores + at, p.dscores ? p.dscores + at : nullptr, p.E, f, wq,
-                                 ((skip >> r) & 0x100u) ? 0x1p64f : (((skip >> r) & 0x10000u) ? 0x1p-64f : 1.f),
-                                 t < hi && ((skip >> r) & 1), nan);
+      const long long at = (long long)(t0 + r * kSide) * p.E;
+      alone += bal_row_alone<LANES>(p.scores + at, p.dscores ? p.dscores + at : nullptr, p.E, f, wq, (left >> r) & 1, nan);
     }
   }
-  return acc;
+  return lane == 0 ? acc + (double)n + alone : 0.0;
 }
 
 // The pass over tokens [t0, t1), sequence by sequence (counts known): the block's share of the loss, for
