@@ -184,7 +184,8 @@ template <int NJ, int VEC, int R, int LANES>
 __device__ __forceinline__ double bal_rows(const BalanceParams& p, int lo, int hi, const float* f, float wq, bool& nan) {
   constexpr int kSide = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LANES - 1), side = (threadIdx.x & 31) / LANES;
-  // D is summed as what the rows' differ from 1 by and their number, in 64 bits: a lane's rows may be thousands
+  // D is summed as the rows' number and what theirs differ from 1 by, in 64 bits but for the R rows of a set: a
+  // lane's sets may be thousands
   double acc = 0, alone = 0;
   int n = 0;
   for (int t0 = lo + warp * R * kSide + side; t0 - side < hi; t0 += kBalThreads / 32 * R * kSide) {
